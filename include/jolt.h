@@ -400,6 +400,151 @@ jolt_status jolt_decode_attn_noalloc(const jolt_shape* shape, const jolt_cell_ch
                                      const void* q, void* out, float* lse, const float* inv_freq,
                                      int32_t pos_offset, void* stream);
 
+/* ---- Tail cache: the tokens that come after the compressed prefill --------------------------------
+ * A stored cache covers the prefill's T tokens. The K and V rows of later tokens are kept in pages,
+ * coded by the codec's residual coder applied to the row itself: x -> y = (1/sqrt(d_h)) H D x
+ * (jolt_rotate_rows with rot_seed), then b bits with an fp16 (scale, zero) per row
+ * (jolt_quantize_pack). Attention of the new tokens over the pages is joined with the stored cache's
+ * by log-sum-exps. The pages hold keys as given: apply RoPE (jolt_rope) before jolt_pages_append.
+ *
+ * One pool per layer holds n_pages pages; a page holds page_size tokens of all KV heads:
+ *   K codes [n_kv][page_size][d_h*b_k/8], K (scale, zero) fp16 [n_kv][page_size][2],
+ *   V codes [n_kv][page_size][d_h*b_v/8], V (scale, zero) fp16 [n_kv][page_size][2],
+ * bits as in the stored cache; pages start at multiples of jolt_pages_layout's page_bytes (a multiple
+ * of 256). The pool must be 16-byte aligned.
+ * Token t of sequence s is row t % page_size of page table[s*max_pages + t / page_size]
+ * (table: device int32 [batch][max_pages]; entries past a sequence's tokens are not read).
+ * lens: device int32 [batch], tokens each sequence holds; read when the kernels run, so a captured
+ * graph follows them. Sequences may share the pages they read, not the pages they write.
+ *
+ * Device-side checks: a length outside [0, max_pages*page_size] is clamped, a table entry outside
+ * [0, n_pages) makes its page's tokens invisible (reads, attention) or unwritten (append); both
+ * set JOLT_ERR_INVALID_ARG in the error word. err (device int32, may be NULL) as in
+ * jolt_quantize_pack: set, never cleared. A call with batch, n_new or n_out 0 returns JOLT_OK. */
+typedef struct {
+  int32_t n_pages;      /* pages in the pool >= 1 */
+  int32_t page_size;    /* tokens per page: 16, 32, 64 or 128 */
+  int32_t n_kv;         /* KV heads >= 1 */
+  int32_t d_h;          /* head dimension: 64 or 128 */
+  int32_t b_k, b_v;     /* bits per key / value element: 2, 4 or 8 */
+  int32_t io_dtype;     /* jolt_dtype of q, k, v and out */
+  uint64_t rot_seed;    /* seed of the rotation's sign diagonal */
+} jolt_pages;
+
+/* Page layout (host): byte offsets of K codes, K (scale, zero), V codes, V (scale, zero) in a page
+ * (offsets may be NULL), and the page's bytes (may be NULL). JOLT_ERR_INVALID_ARG on a bad pages. */
+jolt_status jolt_pages_layout(const jolt_pages* pages, uint64_t offsets[4], uint64_t* page_bytes);
+
+/* Bytes of the pool, n_pages * page_bytes (0 on a bad pages). */
+uint64_t jolt_pages_bytes(const jolt_pages* pages);
+
+/* Codes new rows into the pages as they are written: row i < counts[s] of sequence s is stored as token
+ * lens[s] + i, for K and V. lens is not changed.
+ *   k, v     device [batch][n_src][n_kv][d_h] io dtype, heads contiguous, element strides stride_b
+ *            (sequence) and stride_t (token), the same for both, multiples of 8; 16-byte aligned
+ *   counts   device int32 [batch], rows to write of each sequence (NULL: n_new of every one); clamped
+ *            to [0, n_new]
+ *   src      device int32 [batch][n_new]: the row of k, v that row i takes (the accepted path of a
+ *            drafted tree); NULL: row i. An entry outside [0, n_src) is an error and not written.
+ *   err      also set to JOLT_ERR_NUMERIC for a non-finite row, scale or zero
+ * n_new <= n_src when src is NULL. Rows past the table's capacity are an error and not written.
+ * Asynchronous on `stream`. */
+jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, const int32_t* table, int32_t max_pages,
+                              const int32_t* lens, int32_t batch, int32_t n_new, const int32_t* counts,
+                              const int32_t* src, int32_t n_src, const void* k, const void* v, int64_t stride_b,
+                              int64_t stride_t, int32_t* err, void* stream);
+
+/* Reads pages back to dense rows: token start[s] + i (i < n_out) of sequence s, where it is below
+ * lens[s], into row i of k_out and v_out; other rows are left as they were.
+ *   start    device int32 [batch] >= 0 (NULL: 0; a negative one is an error and reads nothing)
+ *   k_out, v_out  device [batch][n_kv][n_out][d_h] io dtype, rows contiguous, element strides stride_b
+ *            (sequence) and stride_h (head), multiples of 8, 16-byte aligned; either may be NULL. With a
+ *            layer's strides of jolt_compress's K and V this folds a tail into a stored cache's input.
+ * Asynchronous on `stream`. */
+jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
+                            const int32_t* lens, int32_t batch, const int32_t* start, int32_t n_out, void* k_out,
+                            void* v_out, int64_t stride_b, int64_t stride_h, int32_t* err, void* stream);
+
+/* Ancestor masks of a drafted tree (host): parents[i] < i, or -1 for a root; mask[i] has bit j set when j
+ * is i or an ancestor of i. n <= 64. JOLT_ERR_INVALID_ARG on a parent that is not earlier. */
+jolt_status jolt_tree_mask(const int32_t* parents, int32_t n, uint64_t* mask);
+
+/* Workspace bytes of jolt_tree_attn (0 on bad arguments). */
+size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t n_new, int32_t n_q,
+                                int32_t max_pages);
+
+/* Attention of n_new drafted tokens per sequence (1: plain decoding) over the sequence's pages, the
+ * drafted tokens' own K and V under a mask, and a partial result over tokens held elsewhere (a stored
+ * cache through jolt_decode_attn). With s_t = attn_scale * q.k_t over all visible tokens,
+ * out = sum softmax(s)_t v_t and lse = log sum exp(s_t). A row that sees nothing gets out 0, lse -inf.
+ *   q        device [batch][n_new][n_q][d_h] io dtype, heads contiguous, element strides q_stride_b and
+ *            q_stride_t, multiples of 8; 16-byte aligned; n_q a multiple of n_kv, n_new <= 64
+ *   k, v     device [batch][n_new][n_kv][d_h] io dtype, the drafted tokens' rows, strides kv_stride_b and
+ *            kv_stride_t as in jolt_pages_append; both NULL: the drafted tokens see the pages and the
+ *            prefix alone
+ *   mask     device uint64 [batch][n_new]: token i sees drafted token j when bit j of mask[i] is set
+ *            (jolt_tree_mask); NULL: j <= i. A masked row of k or v is never used, whatever it holds.
+ *   counts   device int32 [batch]: drafted tokens of each sequence (NULL: n_new); clamped to [0, n_new].
+ *            Rows of out and lse from counts[s] on are left as they were, rows of k and v are not used.
+ *   prefix_out, prefix_lse  device, layouts of out and lse: the partial result to join (both or
+ *            neither NULL; a lse of -inf: nothing). May be out and lse themselves.
+ *   out      device [batch][n_new][n_q][d_h] io dtype, contiguous, 16-byte aligned
+ *   lse      device fp32 [batch][n_new][n_q], or NULL
+ *   ws       device, >= jolt_tree_attn_workspace, 256-byte aligned, its first 4 bytes zero before the
+ *            first call (the error word, read by jolt_check); calls sharing a ws must not overlap in time
+ * Scores and softmax statistics are fp32. Asynchronous on `stream`. */
+jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
+                           const int32_t* lens, int32_t batch, int32_t n_new, int32_t n_q, const int32_t* counts,
+                           const uint64_t* mask, const void* q, int64_t q_stride_b, int64_t q_stride_t,
+                           const void* k, const void* v, int64_t kv_stride_b, int64_t kv_stride_t,
+                           float attn_scale, const void* prefix_out, const float* prefix_lse, void* out, float* lse,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Which elements of a head form a rotated pair: JOLT_ROPE_HALF (i, i + rot_dim/2), the layout of
+ * jolt_decode_attn's pre-RoPE keys; JOLT_ROPE_INTERLEAVED (2i, 2i + 1). */
+typedef enum { JOLT_ROPE_HALF = 0, JOLT_ROPE_INTERLEAVED = 1 } jolt_rope_layout;
+
+/* Rotary positions of queries and keys in one launch: for pair i of every head of token t, with
+ * angle pos[t] * inv_freq[i], c = scaling * cos, s = scaling * sin:
+ *   (a, b) -> (a c - b s, b c + a s),  inverse: (a c + b s, b c - a s),
+ * the transpose: the gradient of the forward call, and with scaling 1 its inverse. Elements from rot_dim
+ * on are copied. Angles are formed and reduced in double precision, at any int32 position.
+ *   q, q_out   device [n_tokens][n_q][d_h] io dtype, heads contiguous, element strides per token
+ *              >= n_q*d_h; q_out may be q (same stride), and must not overlap it otherwise. n_q may be
+ *              0 (then q, q_out NULL).
+ *   k, k_out   the same with n_kv
+ *   d_h        even, 2..512; rot_dim even, 2..d_h
+ *   pos        device int32 [n_tokens];  inv_freq device fp32 [rot_dim/2], may carry RoPE scaling
+ * Asynchronous on `stream`. */
+jolt_status jolt_rope(const void* q, void* q_out, int32_t n_q, int64_t q_stride, int64_t q_out_stride, const void* k,
+                      void* k_out, int32_t n_kv, int64_t k_stride, int64_t k_out_stride, int64_t n_tokens,
+                      int32_t d_h, int32_t rot_dim, int32_t layout, const int32_t* pos, const float* inv_freq,
+                      float scaling, int32_t inverse, int32_t io_dtype, void* stream);
+
+/* Inverse frequencies f_i = theta^(-2i/rot_dim) scaled for contexts longer than trained (host):
+ *   JOLT_ROPE_PLAIN   f_i
+ *   JOLT_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   JOLT_ROPE_NTK     theta' = theta * factor^(rot_dim/(rot_dim-2)): the lowest frequency is divided by
+ *                     factor, the highest kept
+ *   JOLT_ROPE_RAMP    f_i / factor where a pair turns less than `low` times over original_len tokens, f_i
+ *                     where it turns more than `high` times, and between them
+ *                     (1-w) f_i/factor + w f_i, w = (turns - low)/(high - low)
+ *   JOLT_ROPE_YARN    as RAMP, the ramp linear in the pair index between the (rounded) indices whose pairs
+ *                     turn `high` and `low` times, and scaling_out = 0.1 ln(factor) + 1
+ * inv_freq (host fp32 [rot_dim/2]); scaling_out (host, may be NULL): what to pass as jolt_rope's scaling
+ * and rope_attention_scaling, 1 except for YARN. theta > 0 (> 1 for YARN); rot_dim even, 2..512 (>= 4 for
+ * NTK); factor >= 1; 0 < low < high and original_len >= 1 for RAMP and YARN. JOLT_ERR_INVALID_ARG
+ * otherwise. */
+typedef enum {
+  JOLT_ROPE_PLAIN = 0,
+  JOLT_ROPE_LINEAR = 1,
+  JOLT_ROPE_NTK = 2,
+  JOLT_ROPE_RAMP = 3,
+  JOLT_ROPE_YARN = 4
+} jolt_rope_scaling;
+jolt_status jolt_rope_freqs(int32_t rot_dim, double theta, int32_t mode, double factor, int32_t original_len,
+                            double low, double high, float* inv_freq, float* scaling_out);
+
 /* Per-kernel-family device timing (off by default). When enabled, the library records a CUDA event
  * pair on the launching stream around every launch of the families below and accumulates the
  * elapsed device time together with the launch's algorithmic work (FLOPs of a contraction, or

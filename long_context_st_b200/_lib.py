@@ -44,6 +44,11 @@ class CellChoice(C.Structure):
     _fields_ = [("r_T", C.c_int32), ("r_d", C.c_int32), ("b", C.c_int32)]
 
 
+class Pages(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_kv", C.c_int32), ("d_h", C.c_int32),
+                ("b_k", C.c_int32), ("b_v", C.c_int32), ("io_dtype", C.c_int32), ("rot_seed", C.c_uint64)]
+
+
 # (name, restype, argtypes) of every entry point declared in include/jolt.h
 _P = C.c_void_p
 SIGNATURES = [
@@ -101,6 +106,21 @@ SIGNATURES = [
     ("jolt_sym_eig_workspace", C.c_size_t, [C.c_int32, C.c_int32]),
     ("jolt_stats_enable", None, [C.c_int32]),
     ("jolt_stats_read", C.c_int, [C.POINTER(KernelStat), C.c_int32]),
+    ("jolt_pages_layout", C.c_int, [C.POINTER(Pages), C.POINTER(C.c_uint64), C.POINTER(C.c_uint64)]),
+    ("jolt_pages_bytes", C.c_uint64, [C.POINTER(Pages)]),
+    ("jolt_pages_append", C.c_int, [C.POINTER(Pages), _P, _P, C.c_int32, _P, C.c_int32, C.c_int32, _P, _P, C.c_int32,
+                                    _P, _P, C.c_int64, C.c_int64, _P, _P]),
+    ("jolt_pages_read", C.c_int, [C.POINTER(Pages), _P, _P, C.c_int32, _P, C.c_int32, _P, C.c_int32, _P, _P,
+                                  C.c_int64, C.c_int64, _P, _P]),
+    ("jolt_tree_mask", C.c_int, [_P, C.c_int32, _P]),
+    ("jolt_tree_attn_workspace", C.c_size_t, [C.POINTER(Pages), C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
+    ("jolt_tree_attn", C.c_int, [C.POINTER(Pages), _P, _P, C.c_int32, _P, C.c_int32, C.c_int32, C.c_int32, _P, _P,
+                                 _P, C.c_int64, C.c_int64, _P, _P, C.c_int64, C.c_int64, C.c_float, _P, _P, _P, _P,
+                                 _P, C.c_size_t, _P]),
+    ("jolt_rope", C.c_int, [_P, _P, C.c_int32, C.c_int64, C.c_int64, _P, _P, C.c_int32, C.c_int64, C.c_int64,
+                            C.c_int64, C.c_int32, C.c_int32, C.c_int32, _P, _P, C.c_float, C.c_int32, C.c_int32, _P]),
+    ("jolt_rope_freqs", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.c_double, C.c_int32, C.c_double, C.c_double,
+                                  _P, _P]),
     ("jolt_sym_eig", C.c_int, [_P, C.c_int32, C.c_int32, _P, _P, _P, C.c_size_t, _P]),
 ]
 

@@ -8,7 +8,7 @@ import math
 import numpy as np
 import torch
 
-from ._lib import (lib, check, Shape, CellChoice, JOLT_F32, JOLT_BF16, JOLT_OP_COMPRESS,
+from ._lib import (lib, check, Shape, CellChoice, Pages, JOLT_F32, JOLT_BF16, JOLT_OP_COMPRESS,
                    JOLT_OP_DECODE, JoltError)
 
 _DT = {"f32": JOLT_F32, "bf16": JOLT_BF16}
@@ -20,6 +20,11 @@ def _stream(stream=None):
     if torch.cuda.is_available():
         return C.c_void_p(torch.cuda.current_stream().cuda_stream)
     return C.c_void_p(0)
+
+
+def _raw(stream=None):
+    """The stream as a plain integer (the current one by default)."""
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream
 
 
 def _ptr(t):
@@ -369,6 +374,210 @@ def sym_eig(A, stream=None):
     return (ev, V) if batched else (ev[0], V[0])
 
 
+# ---- tail cache ---------------------------------------------------------------------------------
+# Tensors are checked here (type, shape, strides, device); sizes and options by the library.
+
+_TORCH = {JOLT_F32: torch.float32, JOLT_BF16: torch.bfloat16}
+PAGE_SIZES = (16, 32, 64, 128)
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "ramp": 3, "yarn": 4}
+
+
+def _bad(what):
+    raise JoltError(-1, what)
+
+
+def _dev(t, dtype, shape, what, dev, inner=None):
+    """Address of a device tensor of this type and shape (None: 0). inner: how many trailing
+    dimensions must be contiguous (None: all)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device.index != dev or t.device.type != "cuda":
+        _bad(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, wanted {tuple(shape)} {dtype} on cuda:{dev}")
+    if not t.is_contiguous():
+        if inner is None:
+            _bad(f"{what} is not contiguous")
+        want = 1
+        for i in range(1, inner + 1):
+            if t.stride(-i) != want and t.shape[-i] != 1:
+                _bad(f"{what}: strides {t.stride()}")
+            want *= t.shape[-i]
+    return t.data_ptr()
+
+
+def _steps(t, need):
+    """Strides of the first two dimensions; one of length 1 has the stride a contiguous tensor has."""
+    s1 = t.stride(1) if t.shape[1] > 1 else need
+    return (t.stride(0) if t.shape[0] > 1 else s1 * t.shape[1]), s1
+
+
+def _here(pages, pool, table, lens):
+    dev = torch.cuda.current_device()
+    if table.dim() != 2 or lens.dim() != 1 or pool.dim() != 1:
+        _bad("pool [bytes], table [batch, max_pages] and lens [batch] are wanted")
+    b, mp = table.shape
+    if pool.numel() < pages._bytes:
+        _bad(f"pool of {pool.numel()} bytes, {pages._bytes} are wanted")
+    return (dev, b, mp, _dev(pool, torch.uint8, pool.shape, "pool", dev),
+            _dev(table, torch.int32, table.shape, "table", dev), _dev(lens, torch.int32, (b,), "lens", dev))
+
+
+def make_pages(n_pages, page_size, n_kv, d_h, b_k, b_v, io_dtype="bf16", rot_seed=0) -> Pages:
+    """Description of a tail cache's pages (jolt_pages); raises when the library cannot serve it."""
+    p = Pages(n_pages, page_size, n_kv, d_h, b_k, b_v, _DT[io_dtype], rot_seed)
+    p._bytes = int(lib().jolt_pages_bytes(C.byref(p)))
+    if p._bytes == 0:
+        raise JoltError(-1, "jolt_pages")
+    p._ref, p._dtype = C.byref(p), _TORCH[p.io_dtype]
+    return p
+
+
+def pages_layout(p: Pages):
+    """(offsets of K codes, K (scale, zero), V codes, V (scale, zero) in a page, bytes of a page)."""
+    off = (C.c_uint64 * 4)()
+    n = C.c_uint64(0)
+    check(lib().jolt_pages_layout(C.byref(p), off, C.byref(n)), "jolt_pages_layout")
+    return tuple(off), int(n.value)
+
+
+def pages_bytes(p: Pages) -> int:
+    return p._bytes
+
+
+def new_pool(p: Pages, device="cuda"):
+    return torch.zeros(p._bytes, dtype=torch.uint8, device=device)
+
+
+def pages_append(p: Pages, pool, table, lens, k, v, counts=None, src=None, n_new=None, err=None, stream=None):
+    """Codes rows of k, v [batch, n_src, n_kv, d_h] into the pages, row i of sequence s as its token
+    lens[s] + i, for i < counts[s] (default n_new: src's width, or n_src). src [batch, n_new]: which
+    row of k, v each takes. lens is not changed. err: int32 [1], set on a device-side error."""
+    dev, b, mp, pool_, table_, lens_ = _here(p, pool, table, lens)
+    if k.dim() != 4:
+        _bad("k [batch, n_src, n_kv, d_h] is wanted")
+    n_src = k.shape[1]
+    n = n_new if n_new is not None else n_src if src is None else src.shape[1]
+    shape = (b, n_src, p.n_kv, p.d_h)
+    k_, v_ = _dev(k, p._dtype, shape, "k", dev, 2), _dev(v, p._dtype, shape, "v", dev, 2)
+    s0, s1 = _steps(k, p.n_kv * p.d_h)
+    if _steps(v, p.n_kv * p.d_h) != (s0, s1):
+        _bad("k and v have different strides")
+    check(lib().jolt_pages_append(p._ref, pool_, table_, mp, lens_, b, n, _dev(counts, torch.int32, (b,), "counts", dev),
+                                  _dev(src, torch.int32, (b, n), "src", dev), n_src, k_, v_, s0, s1,
+                                  _dev(err, torch.int32, (1,), "err", dev), _raw(stream)), "jolt_pages_append")
+
+
+def pages_read(p: Pages, pool, table, lens, k_out=None, v_out=None, start=None, err=None, stream=None):
+    """Reads tokens start[s] + i < lens[s] (start: default 0) into k_out and v_out [batch, n_kv, n_out,
+    d_h], as dense rows; other rows are left as they were."""
+    dev, b, mp, pool_, table_, lens_ = _here(p, pool, table, lens)
+    o = k_out if k_out is not None else v_out
+    if o is None or o.dim() != 4:
+        _bad("k_out or v_out [batch, n_kv, n_out, d_h] is wanted")
+    n = o.shape[2]
+    shape = (b, p.n_kv, n, p.d_h)
+    k_, v_ = _dev(k_out, p._dtype, shape, "k_out", dev, 2), _dev(v_out, p._dtype, shape, "v_out", dev, 2)
+    s0, s1 = _steps(o, n * p.d_h)
+    if k_out is not None and v_out is not None and _steps(v_out, n * p.d_h) != (s0, s1):
+        _bad("k_out and v_out have different strides")
+    check(lib().jolt_pages_read(p._ref, pool_, table_, mp, lens_, b, _dev(start, torch.int32, (b,), "start", dev), n,
+                                k_, v_, s0, s1, _dev(err, torch.int32, (1,), "err", dev), _raw(stream)),
+          "jolt_pages_read")
+
+
+def tree_mask(parents):
+    """Ancestor masks uint64 [n] of a drafted tree: parents[i] < i, or -1 for a root."""
+    a = np.ascontiguousarray(parents, dtype=np.int32)
+    out = np.zeros(a.size, dtype=np.uint64)
+    check(lib().jolt_tree_mask(a.ctypes.data, a.size, out.ctypes.data), "jolt_tree_mask")
+    return out
+
+
+def new_tree_workspace(p: Pages, batch, n_new, n_q, max_pages, device="cuda"):
+    n = int(lib().jolt_tree_attn_workspace(C.byref(p), batch, n_new, n_q, max_pages))
+    if n == 0:
+        raise JoltError(-1, "jolt_tree_attn_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def tree_attn(p: Pages, pool, table, lens, q, out, ws, k=None, v=None, mask=None, counts=None, lse=None,
+              prefix_out=None, prefix_lse=None, attn_scale=None, stream=None):
+    """Attention of q [batch, n_new, n_q, d_h] (n_new <= 64 drafted tokens a sequence) over the pages,
+    the drafted tokens' own k, v [batch, n_new, n_kv, d_h] under mask (int64 / uint64 [batch, n_new],
+    default: earlier tokens and itself), and a partial result prefix_out / prefix_lse over tokens held
+    elsewhere (decode_attn's out and lse). Writes out [batch, n_new, n_q, d_h] and lse. attn_scale:
+    default 1/sqrt(d_h). ws: new_tree_workspace; check_ws reports device-side errors."""
+    dev, b, mp, pool_, table_, lens_ = _here(p, pool, table, lens)
+    if q.dim() != 4:
+        _bad("q [batch, n_new, n_q, d_h] is wanted")
+    n, nq = q.shape[1], q.shape[2]
+    dt, rows = p._dtype, (b, n, nq)
+    q_ = _dev(q, dt, (b, n, nq, p.d_h), "q", dev, 2)
+    q0, q1 = _steps(q, nq * p.d_h)
+    k_ = v_ = None
+    k0 = k1 = 0
+    if k is not None or v is not None:
+        if k is None or v is None:
+            _bad("k and v go together")
+        shape = (b, n, p.n_kv, p.d_h)
+        k_, v_ = _dev(k, dt, shape, "k", dev, 2), _dev(v, dt, shape, "v", dev, 2)
+        k0, k1 = _steps(k, p.n_kv * p.d_h)
+        if _steps(v, p.n_kv * p.d_h) != (k0, k1):
+            _bad("k and v have different strides")
+    if mask is not None and mask.dtype not in (torch.int64, torch.uint64):
+        _bad("mask is int64 or uint64")
+    check(lib().jolt_tree_attn(
+        p._ref, pool_, table_, mp, lens_, b, n, nq, _dev(counts, torch.int32, (b,), "counts", dev),
+        None if mask is None else _dev(mask, mask.dtype, (b, n), "mask", dev), q_, q0, q1, k_, v_, k0, k1,
+        1.0 / math.sqrt(p.d_h) if attn_scale is None else attn_scale,
+        _dev(prefix_out, dt, (b, n, nq, p.d_h), "prefix_out", dev), _dev(prefix_lse, torch.float32, rows, "prefix_lse", dev),
+        _dev(out, dt, (b, n, nq, p.d_h), "out", dev), _dev(lse, torch.float32, rows, "lse", dev),
+        _dev(ws, torch.uint8, ws.shape, "ws", dev), ws.numel(), _raw(stream)), "jolt_tree_attn")
+
+
+def rope(q, k, pos, inv_freq, q_out=None, k_out=None, layout="half", scaling=1.0, inverse=False, stream=None):
+    """Rotary positions of q [n_tokens, n_q, d_h] and k [n_tokens, n_kv, d_h] (either may be None) into
+    q_out and k_out (default: new tensors; q_out may be q). pos int32 [n_tokens]; inv_freq fp32
+    [rot_dim / 2]: the first rot_dim elements of each head are rotated. inverse: the transpose, the
+    gradient of the forward call. Returns (q_out, k_out)."""
+    dev = torch.cuda.current_device()
+    one = q if q is not None else k
+    if one is None or pos.dim() != 1 or inv_freq.dim() != 1 or one.dim() != 3 or layout not in ROPE_LAYOUTS:
+        _bad("q, k [n_tokens, heads, d_h], pos [n_tokens], inv_freq [rot_dim / 2] and a layout are wanted")
+    n, d, dt = one.shape[0], one.shape[2], one.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        _bad(f"q, k: {dt}")
+    args = []
+    outs = []
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args += [None, None, 0, 0, 0]
+            outs.append(None)
+            continue
+        if x.dim() != 3:
+            _bad(f"{what} [n_tokens, heads, d_h] is wanted")
+        h = x.shape[1]
+        if y is None:
+            y = torch.empty((n, h, d), dtype=dt, device=x.device)
+        args += [_dev(x, dt, (n, h, d), what, dev, 2), _dev(y, dt, (n, h, d), what + "_out", dev, 2), h,
+                 x.stride(0) if n > 1 else h * d, y.stride(0) if n > 1 else h * d]
+        outs.append(y)
+    check(lib().jolt_rope(*args, n, d, 2 * inv_freq.shape[0], ROPE_LAYOUTS[layout],
+                          _dev(pos, torch.int32, (n,), "pos", dev),
+                          _dev(inv_freq, torch.float32, inv_freq.shape, "inv_freq", dev), scaling, int(inverse),
+                          JOLT_F32 if dt == torch.float32 else JOLT_BF16, _raw(stream)), "jolt_rope")
+    return outs[0], outs[1]
+
+
+def rope_freqs(rot_dim, theta, mode="plain", factor=1.0, original_len=1, low=1.0, high=4.0):
+    """(inv_freq float32 [rot_dim / 2] on the host, scaling) for a long-context scaling (jolt_rope_freqs)."""
+    out = np.zeros(max(rot_dim, 0) // 2, dtype=np.float32)
+    s = C.c_float(0)
+    check(lib().jolt_rope_freqs(rot_dim, theta, ROPE_SCALINGS[mode], factor, original_len, low, high, out.ctypes.data,
+                                C.addressof(s)), "jolt_rope_freqs")
+    return out, s.value
+
+
 def stats_enable(on=True):
     lib().jolt_stats_enable(int(on))
 
@@ -383,7 +592,7 @@ def stats_read(reset=True):
             for i in range(len(KERNEL_FAMILIES))}
 
 
-__all__ = ["analyze_from_host", "layer_align_workspace", "layer_align", "group_layers", "uniform_group", "gemm_bf16_hilo", "gemm_bf16_residual", "allocate_variant", "JOLT_ALLOC_JOINT", "JOLT_ALLOC_KV_SPLIT", "JOLT_ALLOC_UNIFORM", "JOLT_ALLOC_COORD", "GEMM_PLANS", "serialize_cache", "deserialize_cache", "cache_blob_info", "cache_blob_bytes", "decode_attn_noalloc", "stats_enable", "stats_read", "sym_eig", "gemm_bf16", "make_shape", "n_cells", "choices_array", "cell_bytes", "kv_bytes", "cache_layout", "phi",
+__all__ = ["make_pages", "pages_layout", "pages_bytes", "new_pool", "pages_append", "pages_read", "tree_mask", "new_tree_workspace", "tree_attn", "rope", "rope_freqs", "PAGE_SIZES", "ROPE_LAYOUTS", "ROPE_SCALINGS", "analyze_from_host", "layer_align_workspace", "layer_align", "group_layers", "uniform_group", "gemm_bf16_hilo", "gemm_bf16_residual", "allocate_variant", "JOLT_ALLOC_JOINT", "JOLT_ALLOC_KV_SPLIT", "JOLT_ALLOC_UNIFORM", "JOLT_ALLOC_COORD", "GEMM_PLANS", "serialize_cache", "deserialize_cache", "cache_blob_info", "cache_blob_bytes", "decode_attn_noalloc", "stats_enable", "stats_read", "sym_eig", "gemm_bf16", "make_shape", "n_cells", "choices_array", "cell_bytes", "kv_bytes", "cache_layout", "phi",
            "allocate", "workspace_bytes", "new_workspace", "analyze", "compress", "decode_attn",
            "check_ws", "rotate_rows", "quantize_pack", "unpack_dequant", "JoltError",
            "JOLT_OP_COMPRESS", "JOLT_OP_DECODE"]

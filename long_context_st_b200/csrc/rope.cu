@@ -1,0 +1,226 @@
+// jolt_rope: rotary positions of queries and keys.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace jolt {
+namespace {
+
+struct RopeTensor {
+  const void* x;
+  void* y;
+  int64_t sx, sy;  // elements per token
+  int heads;
+};
+struct RopeArgs {
+  RopeTensor t[2];
+  const int32_t* pos;
+  const float* inv_freq;
+  int64_t n_tokens;
+  float scaling;
+  int d, rot, tb, inverse;
+};
+
+constexpr int kThreads = 256;
+
+// (cos, sin) of pos * inv_freq[i] for the block's tokens into cs[token][pair]. The angle is taken in
+// turns in double precision (a float32 product at position 10^5 is off by up to 4e-3 rad), reduced
+// to half a turn either way, and only then rounded.
+__device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t t0, int nt, float2* cs) {
+  const int half = a.rot >> 1;
+  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    double turns = double(a.pos[t0 + t]) * double(a.inv_freq[p]) * 0.15915494309189533577;
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.f * float(turns), &s, &c);
+    cs[i] = make_float2(c * a.scaling, (a.inverse ? -s : s) * a.scaling);
+  }
+  __syncthreads();
+}
+
+template <typename T>
+struct Vec {  // 16 bytes
+  static constexpr int N = 16 / sizeof(T);
+  uint4 raw;
+};
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& r, float (&f)[Vec<T>::N]) {
+  if constexpr (sizeof(T) == 4) {
+    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
+    f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
+  } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::N]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(f[i]);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One pass over q and k: a block takes tb tokens, forms their table once for all heads, and each
+// thread turns 16-byte pieces: half layout, a piece of each half (two loads, two stores);
+// interleaved, one piece of whole pairs. Pieces past rot_dim are copied. x and y may be the same
+// memory: every piece is read and written by one thread.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
+  constexpr int V = Vec<T>::N;
+  extern __shared__ float2 cs[];
+  const int64_t t0 = int64_t(blockIdx.x) * a.tb;
+  const int nt = int(a.n_tokens - t0 < a.tb ? a.n_tokens - t0 : a.tb);
+  rope_table(a, t0, nt, cs);
+  const int half = a.rot >> 1;
+  const int rot_units = HALF ? half / V : a.rot / V;
+  const int units = rot_units + (a.d - a.rot) / V;  // per head
+  const int heads = a.t[0].heads + a.t[1].heads;
+  const int total = nt * heads * units;
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int row = i / units, u = i - row * units;
+    const int t = row / heads;
+    int h = row - t * heads;
+    const int which = h >= a.t[0].heads;
+    const RopeTensor& x = a.t[which];
+    if (which) h -= a.t[0].heads;
+    const T* src = static_cast<const T*>(x.x) + (t0 + t) * x.sx + int64_t(h) * a.d;
+    T* dst = static_cast<T*>(x.y) + (t0 + t) * x.sy + int64_t(h) * a.d;
+    if (u >= rot_units) {
+      const int at = a.rot + (u - rot_units) * V;
+      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
+      continue;
+    }
+    const float2* c = cs + t * half;
+    if (HALF) {
+      const uint4 ra = *reinterpret_cast<const uint4*>(src + u * V);
+      const uint4 rb = *reinterpret_cast<const uint4*>(src + half + u * V);
+      float p[V], q[V], y[V], z[V];
+      unpack<T>(ra, p);
+      unpack<T>(rb, q);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 f = c[u * V + j];
+        y[j] = p[j] * f.x - q[j] * f.y;
+        z[j] = q[j] * f.x + p[j] * f.y;
+      }
+      *reinterpret_cast<uint4*>(dst + u * V) = pack<T>(y);
+      *reinterpret_cast<uint4*>(dst + half + u * V) = pack<T>(z);
+    } else {
+      float p[V], y[V];
+      unpack<T>(*reinterpret_cast<const uint4*>(src + u * V), p);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 f = c[u * (V / 2) + j];
+        y[2 * j] = p[2 * j] * f.x - p[2 * j + 1] * f.y;
+        y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
+      }
+      *reinterpret_cast<uint4*>(dst + u * V) = pack<T>(y);
+    }
+  }
+}
+
+// The same, one pair (or one copied pair) a thread: head sizes, strides or addresses that 16-byte
+// pieces do not divide.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) k_rope_any(const RopeArgs a) {
+  extern __shared__ float2 cs[];
+  const int64_t t0 = int64_t(blockIdx.x) * a.tb;
+  const int nt = int(a.n_tokens - t0 < a.tb ? a.n_tokens - t0 : a.tb);
+  rope_table(a, t0, nt, cs);
+  const int half = a.rot >> 1, pairs = a.d >> 1;
+  const int heads = a.t[0].heads + a.t[1].heads;
+  const int total = nt * heads * pairs;
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    const int row = i / pairs, u = i - row * pairs;
+    const int t = row / heads;
+    int h = row - t * heads;
+    const int which = h >= a.t[0].heads;
+    const RopeTensor& x = a.t[which];
+    if (which) h -= a.t[0].heads;
+    const T* src = static_cast<const T*>(x.x) + (t0 + t) * x.sx + int64_t(h) * a.d;
+    T* dst = static_cast<T*>(x.y) + (t0 + t) * x.sy + int64_t(h) * a.d;
+    if (u >= half) {
+      const T p = src[2 * u], q = src[2 * u + 1];
+      dst[2 * u] = p;
+      dst[2 * u + 1] = q;
+      continue;
+    }
+    const int ia = HALF ? u : 2 * u, ib = HALF ? u + half : 2 * u + 1;
+    const float p = ld_as_float(src, ia), q = ld_as_float(src, ib);
+    const float2 f = cs[t * half + u];
+    st_from_float(dst, ia, p * f.x - q * f.y);
+    st_from_float(dst, ib, q * f.x + p * f.y);
+  }
+}
+
+template <typename T>
+jolt_status launch_rope(const RopeArgs& a, bool half, bool vec, cudaStream_t st) {
+  const unsigned grid = unsigned((a.n_tokens + a.tb - 1) / a.tb);
+  const size_t smem = size_t(a.tb) * (a.rot / 2) * sizeof(float2);
+  if (vec) {
+    if (half) k_rope_vec<T, true><<<grid, kThreads, smem, st>>>(a);
+    else k_rope_vec<T, false><<<grid, kThreads, smem, st>>>(a);
+  } else {
+    if (half) k_rope_any<T, true><<<grid, kThreads, smem, st>>>(a);
+    else k_rope_any<T, false><<<grid, kThreads, smem, st>>>(a);
+  }
+  JOLT_CUDA_TRY(cudaGetLastError());
+  return JOLT_OK;
+}
+
+}  // namespace
+}  // namespace jolt
+
+using namespace jolt;
+
+extern "C" jolt_status jolt_rope(const void* q, void* q_out, int32_t n_q, int64_t q_stride, int64_t q_out_stride,
+                                 const void* k, void* k_out, int32_t n_kv, int64_t k_stride, int64_t k_out_stride,
+                                 int64_t n_tokens, int32_t d_h, int32_t rot_dim, int32_t layout, const int32_t* pos,
+                                 const float* inv_freq, float scaling, int32_t inverse, int32_t io_dtype,
+                                 void* stream) {
+  if (n_q < 0 || n_kv < 0 || n_q > 65536 || n_kv > 65536 || n_q + n_kv < 1 || n_tokens < 0)
+    return JOLT_ERR_INVALID_ARG;
+  if (d_h < 2 || d_h > 512 || d_h % 2 || rot_dim < 2 || rot_dim > d_h || rot_dim % 2) return JOLT_ERR_INVALID_ARG;
+  if (layout != JOLT_ROPE_HALF && layout != JOLT_ROPE_INTERLEAVED) return JOLT_ERR_INVALID_ARG;
+  if (io_dtype != JOLT_F32 && io_dtype != JOLT_BF16) return JOLT_ERR_INVALID_ARG;
+  if (!(scaling - scaling == 0.f) || (inverse != 0 && inverse != 1)) return JOLT_ERR_INVALID_ARG;
+  if (n_tokens == 0) return JOLT_OK;
+  if (!pos || !inv_freq || (n_q && (!q || !q_out)) || (n_kv && (!k || !k_out))) return JOLT_ERR_INVALID_ARG;
+  if (n_tokens > (int64_t(1) << 31)) return JOLT_ERR_INVALID_ARG;
+  RopeArgs a{};
+  a.t[0] = RopeTensor{q, q_out, q_stride, q_out_stride, n_q};
+  a.t[1] = RopeTensor{k, k_out, k_stride, k_out_stride, n_kv};
+  const int e = io_dtype == JOLT_F32 ? 4 : 2, v = 16 / e;
+  bool vec = (layout == JOLT_ROPE_HALF ? rot_dim / 2 : rot_dim) % v == 0 && d_h % v == 0;
+  for (const RopeTensor& t : a.t) {
+    if (!t.heads) continue;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(t.x), y = reinterpret_cast<uintptr_t>(t.y);
+    if (t.sx < int64_t(t.heads) * d_h || t.sy < int64_t(t.heads) * d_h || x % e || y % e) return JOLT_ERR_INVALID_ARG;
+    if (x == y && t.sx != t.sy && n_tokens > 1) return JOLT_ERR_INVALID_ARG;
+    vec = vec && x % 16 == 0 && y % 16 == 0 && t.sx % v == 0 && t.sy % v == 0;
+  }
+  a.pos = pos;
+  a.inv_freq = inv_freq;
+  a.n_tokens = n_tokens;
+  a.scaling = scaling;
+  a.d = d_h;
+  a.rot = rot_dim;
+  a.inverse = inverse;
+  a.tb = 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return io_dtype == JOLT_F32 ? launch_rope<float>(a, layout == JOLT_ROPE_HALF, vec, st)
+                              : launch_rope<__nv_bfloat16>(a, layout == JOLT_ROPE_HALF, vec, st);
+}

@@ -1,0 +1,768 @@
+// jolt_tree_attn: attention of drafted tokens over the tail cache's pages.
+//
+// With y = R k the stored (rotated) key, q.k = (R q).y, and y_j = scale * c_j + zero with whole
+// codes c_j, so a score needs one product of (R q) with the codes themselves:
+//   s = scale * ((R q).(c - o)) + (zero + o * scale) * sum(R q),   o = 2^(b-1) (codes centred at 0).
+// The same for values: sum_t p_t y_t = sum_t (p_t scale_t) (c_t - o) + sum_t p_t (zero_t + o scale_t),
+// whose second term is one number for all features; R^T is applied once, to the sum.
+//
+// Codes are exact in f16, so they feed m16n8k16 MMAs straight from their bits; what is rounded is
+// the other operand: R q is carried as two f16 terms (22 bits: the log-sum-exp stays fp32-accurate),
+// p * scale as one f16 term for bf16 output (11 bits, against the 8 the output keeps) and as two for
+// fp32. Both are first scaled by powers of two into f16's normal range: R q by its row's largest
+// element, p * scale by the largest value scale met so far.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "pages_codes.cuh"
+#include "sm100.cuh"
+#include "pages.cuh"
+
+namespace jolt {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 32;        // tokens a warp takes at a time
+constexpr int kMaxSplits = 63;   // + the drafted tokens' own partial: two per lane in the merge
+constexpr int kMaxDraft = 64;    // bits of a mask word
+constexpr int kMaxStages = 4;
+
+struct TreeArgs {
+  PagesDev p;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t qsb, qst, ksb, kst;
+  const int32_t* counts;
+  const uint64_t* mask;
+  const void* prefix_out;
+  const float* prefix_lse;
+  void* out;
+  float* lse;
+  float2* ml;   // [rows][parts] (maximum in log2 units, sum)
+  float* acc;   // [rows][parts][D]
+  int32_t* err;
+  float scale2;  // attn_scale * log2(e): scores are kept in log2 units
+  int n_new, n_q, gq, splits, parts, batch, blocks, stages, stage_bytes;
+};
+
+__device__ __forceinline__ int draft_count(const TreeArgs& a, int b) {
+  return a.counts ? min(max(a.counts[b], 0), a.n_new) : a.n_new;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2_pack(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 h2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// Keys of one tile: acc[grp][nt] += codes (tokens grp*16 + {g, g+8}) x R q (columns of tile nt).
+template <int D, int B, int NT, int QT>
+__device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, int lane, float (&s)[2][NT][4]) {
+  constexpr int W = D * B / 128;  // words of a lane's quarter row
+  const int g = lane >> 2, m = lane & 3;
+  uint32_t w[4][W];  // rows g, g+8, g+16, g+24
+#pragma unroll
+  for (int r = 0; r < 4; ++r) load_words<W>(kc + (g + 8 * r) * (D * B / 8) + m * (4 * W), w[r]);
+#pragma unroll
+  for (int st = 0; st < D / 16; ++st) {
+    uint32_t a0[4], a1[4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      a0[2 * x] = code_pair<B, W>(w[0], 2 * st + x);
+      a0[2 * x + 1] = code_pair<B, W>(w[1], 2 * st + x);
+      a1[2 * x] = code_pair<B, W>(w[2], 2 * st + x);
+      a1[2 * x + 1] = code_pair<B, W>(w[3], 2 * st + x);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        const uint2 b = qf[((t * NT + nt) * (D / 16) + st) * 32 + lane];
+        mma_f16_16816(s[0][nt], a0, b.x, b.y);
+        mma_f16_16816(s[1][nt], a1, b.x, b.y);
+      }
+  }
+}
+
+// Values of one tile: o[mt][nt] += codes^T (features) x (p scale) (tokens), PT terms of the latter.
+template <int D, int B, int NT, int PT>
+__device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&pf)[PT][2][NT][2], int lane,
+                                            float (&o)[D / 16][NT][4]) {
+  constexpr int CB = D * B / 64;             // bytes of a lane's eighth row
+  constexpr int W = CB >= 4 ? CB / 4 : 1;
+  const int g = lane >> 2, m = lane & 3;
+#pragma unroll
+  for (int grp = 0; grp < 2; ++grp) {
+    uint32_t w[4][W];  // tokens 2m, 2m+1, 2m+8, 2m+9
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t* src = vc + (grp * 16 + 2 * m + (r & 1) + (r >> 1) * 8) * (D * B / 8) + g * CB;
+      if constexpr (CB == 2) w[r][0] = *reinterpret_cast<const uint16_t*>(src);
+      else load_words<W>(src, w[r]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      uint32_t a[4];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        a[f] = code_across<B, W>(w[0], w[1], 2 * mt + f);
+        a[f + 2] = code_across<B, W>(w[2], w[3], 2 * mt + f);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int t = 0; t < PT; ++t) mma_f16_16816(o[mt][nt], a, pf[t][grp][nt][0], pf[t][grp][nt][1]);
+    }
+  }
+}
+
+// The drafted tokens' own keys and values, in fp32 on the CUDA cores (at most 64 keys).
+template <typename T, int D, int RB>
+__device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* smem) {
+  constexpr int E = D / 32, KS = D + 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cnt = draft_count(a, b);
+  const int rows = min(RB, cnt * a.gq - r0);
+  if (rows <= 0) return;
+  float* ks = reinterpret_cast<float*>(smem);           // [cnt][KS]
+  float* vs = ks + kMaxDraft * KS;                      // [cnt][D]
+  float* qs = vs + kMaxDraft * D;                       // [RB][D]
+  float* ps = qs + RB * D;                              // [warp][4][64]
+  const T* kb = static_cast<const T*>(a.k) + int64_t(b) * a.ksb + int64_t(h) * D;
+  const T* vb = static_cast<const T*>(a.v) + int64_t(b) * a.ksb + int64_t(h) * D;
+  for (int i = tid; i < cnt * D; i += kThreads) {
+    const int t = i / D, f = i % D;
+    ks[t * KS + f] = ld_as_float(kb, t * a.kst + f);
+    vs[t * D + f] = ld_as_float(vb, t * a.kst + f);
+  }
+  const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
+  for (int i = tid; i < rows * D; i += kThreads) {
+    const int r = r0 + i / D, f = i % D;
+    qs[i] = ld_as_float(qb, int64_t(r / a.gq) * a.qst + (r % a.gq) * D + f) * a.scale2;
+  }
+  __syncthreads();
+  for (int q0 = warp * 4; q0 < rows; q0 += kWarps * 4) {
+    uint64_t bits[4];
+    float s[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = (r0 + q0 + r) / a.gq;
+      bits[r] = 0;
+      if (q0 + r < rows) bits[r] = a.mask ? a.mask[int64_t(b) * a.n_new + i] : ~uint64_t(0) >> (63 - i);
+      if (cnt < 64) bits[r] &= (uint64_t(1) << cnt) - 1;
+      s[r][0] = s[r][1] = 0.f;
+    }
+    const int j1 = min(lane, cnt - 1), j2 = min(lane + 32, cnt - 1);
+    for (int f = 0; f < D; f += 4) {
+      const float4 k1 = *reinterpret_cast<const float4*>(ks + j1 * KS + f);
+      const float4 k2 = *reinterpret_cast<const float4*>(ks + j2 * KS + f);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(qs + min(q0 + r, rows - 1) * D + f);
+        s[r][0] += x.x * k1.x + x.y * k1.y + x.z * k1.z + x.w * k1.w;
+        s[r][1] += x.x * k2.x + x.y * k2.y + x.z * k2.z + x.w * k2.w;
+      }
+    }
+    float o[4][E];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool v1 = (bits[r] >> lane) & 1, v2 = (bits[r] >> (lane + 32)) & 1;
+      const float s1 = v1 ? s[r][0] : -INFINITY, s2 = v2 ? s[r][1] : -INFINITY;
+      const float mx = warp_max(fmaxf(s1, s2));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      const float p1 = v1 ? exp2f(s1 - ref) : 0.f, p2 = v2 ? exp2f(s2 - ref) : 0.f;
+      const float l = warp_sum(p1 + p2);
+      ps[(warp * 4 + r) * 64 + lane] = p1;
+      ps[(warp * 4 + r) * 64 + lane + 32] = p2;
+      if (lane == 0 && q0 + r < rows) {
+        const int row = r0 + q0 + r;
+        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
+        a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+    }
+    __syncwarp();
+    for (int j = 0; j < cnt; ++j) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = vs[j * D + lane * E + e];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if ((bits[r] >> j) & 1) {  // a masked row of v is not touched: it may hold anything
+          const float p = ps[(warp * 4 + r) * 64 + j];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[r][e] += p * v[e];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (q0 + r < rows) {
+        const int row = r0 + q0 + r;
+        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
+        float* dst = a.acc + (gr * a.parts + a.splits) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[e] = o[r][e];
+      }
+    __syncwarp();
+  }
+}
+
+// Scores, online softmax and values of one split of a sequence's pages for one KV head and up to RB
+// query rows (drafted token x head of the group). The MMAs have tokens (keys) or features (values)
+// as their 16 rows and query rows as their 8 columns, so single-token decoding wastes little; with
+// PACK (at most 4 rows) columns 0-3 carry the first term of R q and 4-7 the second, and the values
+// the two terms of p likewise. Each warp takes 32-token tiles of its own through a ring of bulk
+// copies (one mbarrier a stage); warps meet once, to add up their partial results.
+template <typename T, int D, int NT, bool PACK>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeArgs a) {
+  using namespace sm100;
+  constexpr int RB = PACK ? 4 : 8 * NT;
+  constexpr int QT = PACK ? 1 : 2;
+  constexpr int PT = !PACK && sizeof(T) == 4 ? 2 : 1;
+  constexpr int E = D / 32, NS = D / 16, C = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, m = lane & 3;
+  const int h = blockIdx.y / a.blocks, r0 = (blockIdx.y % a.blocks) * RB, b = blockIdx.z;
+  const int split = blockIdx.x;
+  if (split == a.splits) {
+    draft_block<T, D, RB>(a, b, h, r0, smem);
+    return;
+  }
+  const int cnt = draft_count(a, b);
+  const int rows = min(RB, cnt * a.gq - r0);
+  if (rows <= 0) return;
+
+  uint2* qf = reinterpret_cast<uint2*>(smem);                        // [QT][NT][NS][32]
+  float* rs = reinterpret_cast<float*>(qf + QT * NT * NS * 32);      // [C] 2^-k of R q's scaling
+  float* qsum = rs + C;                                              // [C]
+  float* xm = qsum + C;                                              // [kWarps][C]
+  float* xl = xm + kWarps * C;                                       // [kWarps][C]
+  float* xz = xl + kWarps * C;                                       // [kWarps][C]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xz + kWarps * C);     // [kWarps][kMaxStages]
+  uint32_t* there = reinterpret_cast<uint32_t*>(bars + kWarps * kMaxStages);  // pieces of a stage that hold tokens
+  uint8_t* ring0 = reinterpret_cast<uint8_t*>(there + kWarps * kMaxStages);
+
+  const int len = pages_len(a.p, b, a.err);
+  const int tiles = (len + kTile - 1) / kTile;
+  const int per = (tiles + a.splits - 1) / a.splits;
+  const int t_end = min(tiles, (split + 1) * per);
+  const int t_first = split * per + warp;
+  const int n_mine = t_first < t_end ? (t_end - t_first + kWarps - 1) / kWarps : 0;
+  const int rbk = D * a.p.bk / 8, rbv = D * a.p.bv / 8;
+  uint8_t* ring = ring0 + warp * a.stages * a.stage_bytes;
+  uint32_t bar0 = smem_u32(bars + warp * kMaxStages);
+  if (lane == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  const int pt = min(kTile, 1 << a.p.ps_log2);  // tokens of a piece: a tile spans one or two pages
+  auto fetch = [&](int n) {  // n-th tile of this warp into stage n % stages
+    const int st = n % a.stages;
+    const int piece = lane >> 2, kind = lane & 3;
+    const int tok = (t_first + n * kWarps) * kTile + piece * pt;
+    int page = -1;
+    if (piece * pt < kTile && tok < len) page = page_of(a.p, b, tok, a.err);
+    const uint32_t okm = __ballot_sync(0xffffffffu, page >= 0) & 0x11u;
+    const uint32_t bar = bar0 + 8 * st;
+    if (lane == 0) {
+      there[warp * kMaxStages + st] = okm;
+      mbar_expect_tx(bar, __popc(okm) * pt * (rbk + rbv + 8));
+    }
+    __syncwarp();
+    if (page >= 0) {
+      const uint32_t rb = kind == 0 ? rbk : kind == 2 ? rbv : 4;
+      const uint32_t seg = kind == 0 ? a.p.kc : kind == 1 ? a.p.ks : kind == 2 ? a.p.vc : a.p.vs;
+      const uint32_t at = kind == 0 ? 0 : kind == 1 ? kTile * rbk : kind == 2 ? kTile * (rbk + 4) : kTile * (rbk + 4 + rbv);
+      const uint8_t* src = a.p.pool + uint64_t(page) * a.p.page_bytes + seg +
+                           (uint64_t(h) * (1 << a.p.ps_log2) + (tok & ((1 << a.p.ps_log2) - 1))) * rb;
+      bulk_load(smem_u32(ring + st * a.stage_bytes) + at + piece * pt * rb, src, pt * rb, bar);
+    }
+  };
+  for (int n = 0; n < min(a.stages, n_mine); ++n) fetch(n);
+
+  // R q of this block's rows as MMA operands: lane (g, m) of k-step st holds column g, the features
+  // that the codes of quarter row m give at that step
+  {
+    const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
+    const float isd = rsqrtf(float(D));
+    __half* qh = reinterpret_cast<__half*>(qf);
+    const int nc = 32 / a.p.bk;  // codes of a word
+    for (int r = warp; r < RB; r += kWarps) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+      if (r < rows) {
+        const int row = r0 + r;
+        const T* x = qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = ld_as_float(x, e) * a.scale2;
+      }
+      warp_rotate<E>(v, a.p.seed, isd);
+      float top = 0.f, sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        top = fmaxf(top, fabsf(v[e]));
+        sum += v[e];
+      }
+      top = warp_max(top);
+      sum = warp_sum(sum);
+      // 2^k top in [2^14, 2^15); a zero or non-finite row is left as it is
+      int k = 0;
+      if (top > 0.f && top < INFINITY) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
+      const float up = pow2i(k);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int f = lane * E + e;
+        const int mm = f / (D / 4), fq = f % (D / 4);       // quarter row, feature in it
+        const int w = fq / nc, c = fq % nc;                 // word, code in it
+        const int pair = w * (nc / 2) + c % (nc / 2), hi = c / (nc / 2);
+        const float x = v[e] * up;
+        const __half x1 = __float2half_rn(x);
+        const __half x2 = __float2half_rn(x - __half2float(x1));
+        const int st = pair >> 1, reg = pair & 1;
+        // [term][nt][st][lane = 4 * column + mm][reg][hi]
+        const int at = ((st * 32 + 4 * (r & 7) + mm) * 2 + reg) * 2 + hi;
+        if (PACK) {
+          qh[at] = x1;
+          qh[at + 4 * 4 * 4] = x2;  // column r + 4
+        } else {
+          const int nt = r >> 3;
+          qh[at + nt * NS * 128] = x1;
+          qh[at + (NT + nt) * NS * 128] = x2;
+        }
+      }
+      if (lane == 0) {
+        rs[r] = pow2i(-k);
+        qsum[r] = sum;
+        if (PACK) {
+          rs[r + 4] = pow2i(-k);
+          qsum[r + 4] = sum;
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  float o[NS][NT][4], mx[NT][2], l[NT][2], z[NT][2], crs[NT][2], cqs[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      mx[nt][c] = -INFINITY;
+      l[nt][c] = z[nt][c] = 0.f;
+      crs[nt][c] = rs[nt * 8 + 2 * m + c];
+      cqs[nt][c] = qsum[nt * 8 + 2 * m + c];
+    }
+#pragma unroll
+    for (int mt = 0; mt < NS; ++mt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.f;
+  }
+  int ve = -30;  // value scales met so far are below 2^ve
+  const float ok_off = float(1 << (a.p.bk - 1)), ov_off = float(1 << (a.p.bv - 1));
+  for (int n = 0; n < n_mine; ++n) {
+    const int st = n % a.stages;
+    if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (n / a.stages) & 1, a.err))) {
+      // gave up (reported): wait, with the same limit, for what is still in flight, then stop
+      for (int x = n + 1; x < min(n + a.stages, n_mine); ++x)
+        mbar_wait(bar0 + 8 * (x % a.stages), (x / a.stages) & 1, a.err);
+      break;
+    }
+    const uint8_t* kc = ring + st * a.stage_bytes;
+    const __half2* ksz = reinterpret_cast<const __half2*>(kc + kTile * rbk);
+    const uint8_t* vc = kc + kTile * (rbk + 4);
+    const __half2* vsz = reinterpret_cast<const __half2*>(vc + kTile * rbv);
+    const uint32_t okm = there[warp * kMaxStages + st];
+    const int tok0 = (t_first + n * kWarps) * kTile;
+
+    float s[2][NT][4];
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[grp][nt][c] = 0.f;
+    if (a.p.bk == 4) keys_tile<D, 4, NT, QT>(kc, qf, lane, s);
+    else if (a.p.bk == 8) keys_tile<D, 8, NT, QT>(kc, qf, lane, s);
+    else keys_tile<D, 2, NT, QT>(kc, qf, lane, s);
+
+    // scale, zero and visibility of this lane's four tokens (rows g + 8 i)
+    float vsc[4], vzr[4];
+    bool seen[4];
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = g + 8 * i;
+      seen[i] = tok0 + t < len && ((pt == kTile ? okm : okm >> (4 * (i >> 1))) & 1);
+      const float2 ks = __half22float2(ksz[t]), vs = __half22float2(vsz[t]);
+      vsc[i] = seen[i] ? vs.x : 0.f;
+      vzr[i] = seen[i] ? vs.y + ov_off * vs.x : 0.f;
+      big = max(big, __float_as_uint(fabsf(vsc[i])));
+      const float kz = ks.y + ok_off * ks.x;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& x = s[i >> 1][nt][2 * (i & 1) + c];
+          if (PACK) x += __shfl_xor_sync(0xffffffffu, x, 2);  // the two terms of R q
+          x = seen[i] ? x * crs[nt][c] * ks.x + kz * cqs[nt][c] : -INFINITY;
+        }
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    const int ve_new = max(ve, int(big >> 23) - 126);
+    const float drop = pow2i(max(ve - ve_new, -126));
+    ve = ve_new;
+    const float up = pow2i(15 - ve);
+
+    uint32_t pf[PT][2][NT][2];
+    bool scale_o = drop != 1.f;
+    float al[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float t = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+        const float now = fmaxf(mx[nt][c], t);
+        const float ref = now == -INFINITY ? 0.f : now;
+        al[nt][c] = exp2f(mx[nt][c] - ref);
+        scale_o = scale_o || al[nt][c] != 1.f;
+        mx[nt][c] = now;
+        float sum = 0.f, zs = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float& x = s[i >> 1][nt][2 * (i & 1) + c];
+          const float p = exp2f(x - ref);
+          sum += p;
+          zs += p * vzr[i];
+          x = p * (vsc[i] * up);
+        }
+        l[nt][c] = l[nt][c] * al[nt][c] + sum;
+        z[nt][c] = z[nt][c] * al[nt][c] + zs;
+      }
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x0 = s[grp][nt][2 * i], x1 = s[grp][nt][2 * i + 1];
+          uint32_t hi = h2_pack(x0, x1);
+          if (sizeof(T) == 4) {
+            const float2 f = h2_floats(hi);
+            const uint32_t lo = h2_pack(x0 - f.x, x1 - f.y);
+            if (PACK) hi = m < 2 ? hi : lo;
+            else pf[PT - 1][grp][nt][i] = trans8x8(lo);
+          } else if (PACK) {
+            hi = m < 2 ? hi : 0u;
+          }
+          pf[0][grp][nt][i] = trans8x8(hi);
+        }
+    if (__any_sync(0xffffffffu, scale_o)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float f = al[nt][c] * drop;
+#pragma unroll
+          for (int mt = 0; mt < NS; ++mt) {
+            o[mt][nt][c] *= f;
+            o[mt][nt][c + 2] *= f;
+          }
+        }
+    }
+    if (a.p.bv == 4) values_tile<D, 4, NT, PT>(vc, pf, lane, o);
+    else if (a.p.bv == 8) values_tile<D, 8, NT, PT>(vc, pf, lane, o);
+    else values_tile<D, 2, NT, PT>(vc, pf, lane, o);
+    __syncwarp();  // every lane is done with the stage
+    if (n + a.stages < n_mine) fetch(n + a.stages);
+  }
+  // ---- the warps' partial results into one ----
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+        z[nt][c] += __shfl_xor_sync(0xffffffffu, z[nt][c], x);
+      }
+      if (g == 0) xm[warp * C + nt * 8 + 2 * m + c] = mx[nt][c];
+    }
+  __syncthreads();
+  const float unit = pow2i(ve - 15);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = nt * 8 + 2 * m + c;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, xm[w * C + col]);
+      const float f = mx[nt][c] == -INFINITY ? 0.f : exp2f(mx[nt][c] - top);
+      if (g == 0) {
+        xl[warp * C + col] = l[nt][c] * f;
+        xz[warp * C + col] = z[nt][c] * f;
+      }
+      mx[nt][c] = top;
+#pragma unroll
+      for (int mt = 0; mt < NS; ++mt) {
+        o[mt][nt][c] *= f * unit;
+        o[mt][nt][c + 2] *= f * unit;
+        if (PACK) {
+          o[mt][nt][c] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c], 2);
+          o[mt][nt][c + 2] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c + 2], 2);
+        }
+      }
+    }
+  float* red = reinterpret_cast<float*>(ring0);  // [kWarps / 2][NS * NT * 4][32]
+  constexpr int NR = NS * NT * 4;
+#pragma unroll
+  for (int half = kWarps / 2; half >= 1; half >>= 1) {
+    if (warp >= half && warp < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) red[((warp - half) * NR + i) * 32 + lane] = o[i / (NT * 4)][(i / 4) % NT][i % 4];
+    }
+    __syncthreads();
+    if (warp < half) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) o[i / (NT * 4)][(i / 4) % NT][i % 4] += red[(warp * NR + i) * 32 + lane];
+    }
+    __syncthreads();
+  }
+  if (warp != 0) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = nt * 8 + 2 * m + c;
+      if (col >= rows) continue;
+      float ls = 0.f, zs = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        ls += xl[w * C + col];
+        zs += xz[w * C + col];
+      }
+      const int row = r0 + col;
+      const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
+      const int64_t part = gr * a.parts + split;
+      if (g == 0) a.ml[part] = make_float2(mx[nt][c], ls);
+      if (mx[nt][c] == -INFINITY) continue;
+      float* dst = a.acc + part * D + g * (D / 8);
+#pragma unroll
+      for (int mt = 0; mt < NS; mt += 2)
+        *reinterpret_cast<float4*>(dst + 2 * mt) = make_float4(o[mt][nt][c] + zs, o[mt][nt][c + 2] + zs,
+                                                               o[mt + 1][nt][c] + zs, o[mt + 1][nt][c + 2] + zs);
+    }
+}
+
+// One warp a row: joins the splits, rotates their sum back, then adds the drafted tokens' part and the
+// prefix. Launched while k_tree still runs (its grid starts as k_tree's blocks leave); it waits for
+// k_tree's end before it reads anything.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  float back[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) back[e] = rsqrtf(float(D)) * rot_sign(a.p.seed, lane * E + e);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= int64_t(a.batch) * a.n_new * a.n_q) return;
+  const int64_t bi = row / a.n_q;
+  const int b = int(bi / a.n_new), i = int(bi % a.n_new);
+  if (i >= draft_count(a, b)) return;
+  float2 p[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int s = lane + 32 * x;
+    p[x] = s < a.parts ? a.ml[row * a.parts + s] : make_float2(-INFINITY, 0.f);
+  }
+  const float pre = a.prefix_lse ? a.prefix_lse[row] * 1.4426950408889634f : -INFINITY;
+  const float top = fmaxf(warp_max(fmaxf(p[0].x, p[1].x)), pre);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float w[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) w[x] = exp2f(p[x].x - ref);
+  const float wp = pre == -INFINITY ? 0.f : exp2f(pre - ref);
+  const float sum = warp_sum(w[0] * p[0].y + w[1] * p[1].y) + wp;
+  float o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  const float* acc = a.acc + row * a.parts * D + lane * E;
+  for (int s = 0; s < a.splits; ++s) {
+    const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
+    if (f != 0.f) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(s) * D + e];
+    }
+  }
+  warp_fwht<E>(o);
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] *= back[e];
+  if (draft) {
+    const float f = __shfl_sync(0xffffffffu, a.splits < 32 ? w[0] : w[1], a.splits & 31);
+    if (f != 0.f) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.splits) * D + e];
+    }
+  }
+  if (wp != 0.f) {
+    const T* po = static_cast<const T*>(a.prefix_out) + row * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += wp * ld_as_float(po, e);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* out = static_cast<T*>(a.out) + row * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) st_from_float(out, e, o[e] * inv);
+  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+// ---- host -------------------------------------------------------------------------------------------
+
+struct TreePlan {
+  int nt, blocks, splits, parts, stages, stage_bytes;
+  bool pack;
+  size_t smem, ws_acc, ws_total;
+};
+
+TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_pages) {
+  TreePlan t{};
+  const int rows = n_new * (n_q / p.n_kv);
+  t.pack = rows <= 4;
+  t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  t.blocks = (rows + 8 * t.nt - 1) / (8 * t.nt);
+  const int64_t units = int64_t(batch) * p.n_kv * t.blocks;
+  const int64_t tiles = (int64_t(max_pages) * p.page_size + kTile - 1) / kTile;
+  const int resident = 148 * (t.nt == 1 ? 2 : 1);
+  t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + kWarps - 1) / kWarps, resident / units})));
+  t.parts = t.splits + 1;
+  t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
+  const int budget = (t.nt == 1 ? 100 : 190) * 1024;
+  t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
+  const int C = 8 * t.nt, qt = t.pack ? 1 : 2;
+  const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 8 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
+  const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
+  const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
+  const size_t draft = size_t(kMaxDraft) * (2 * p.d_h + 4) * 4 + size_t(t.pack ? 4 : C) * p.d_h * 4 + kWarps * 4 * 64 * 4;
+  t.smem = std::max(head + std::max(ring, red), draft);
+  const size_t nrows = size_t(batch) * n_new * n_q;
+  t.ws_acc = align_up(sizeof(WsHeader) + nrows * t.parts * sizeof(float2), 256);
+  t.ws_total = align_up(t.ws_acc + nrows * t.parts * p.d_h * sizeof(float), 256);
+  return t;
+}
+
+bool tree_dims_ok(const jolt_pages* p, int batch, int n_new, int n_q, int max_pages) {
+  return pages_ok(p) && batch >= 0 && batch <= 65535 && n_new >= 0 && n_new <= kMaxDraft && n_q >= p->n_kv &&
+         n_q % p->n_kv == 0 && n_q <= 65536 && max_pages >= 1 && int64_t(max_pages) * p->page_size <= (int64_t(1) << 24);
+}
+
+template <typename T, int D, int NT, bool PACK>
+jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
+  JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree<T, D, NT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(t.smem)));
+  const dim3 grid(t.splits + (draft ? 1 : 0), a.p.n_kv * t.blocks, a.batch);
+  k_tree<T, D, NT, PACK><<<grid, kThreads, t.smem, st>>>(a);
+  JOLT_CUDA_TRY(cudaGetLastError());
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned((int64_t(a.batch) * a.n_new * a.n_q + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  JOLT_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tree_merge<T, D>, a, draft));
+  return JOLT_OK;
+}
+
+template <typename T, int D>
+jolt_status launch_tree_d(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
+  if (t.pack) return launch_tree<T, D, 1, true>(a, t, draft, st);
+  if (t.nt == 1) return launch_tree<T, D, 1, false>(a, t, draft, st);
+  if (t.nt == 2) return launch_tree<T, D, 2, false>(a, t, draft, st);
+  return launch_tree<T, D, 4, false>(a, t, draft, st);
+}
+
+bool rows_ok(const void* x, int64_t s0, int64_t s1) {
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
+}
+
+}  // namespace
+}  // namespace jolt
+
+using namespace jolt;
+
+extern "C" size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t n_new, int32_t n_q,
+                                           int32_t max_pages) {
+  if (!tree_dims_ok(pages, batch, n_new, n_q, max_pages)) return 0;
+  return tree_plan(*pages, std::max(batch, 1), std::max(n_new, 1), n_q, max_pages).ws_total;
+}
+
+extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table,
+                                      int32_t max_pages, const int32_t* lens, int32_t batch, int32_t n_new,
+                                      int32_t n_q, const int32_t* counts, const uint64_t* mask, const void* q,
+                                      int64_t q_stride_b, int64_t q_stride_t, const void* k, const void* v,
+                                      int64_t kv_stride_b, int64_t kv_stride_t, float attn_scale,
+                                      const void* prefix_out, const float* prefix_lse, void* out, float* lse,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  if (!tree_dims_ok(pages, batch, n_new, n_q, max_pages)) return JOLT_ERR_INVALID_ARG;
+  if (!(attn_scale > 0.f) || !(attn_scale < INFINITY)) return JOLT_ERR_INVALID_ARG;
+  if (batch == 0 || n_new == 0) return JOLT_OK;
+  if (!pool || reinterpret_cast<uintptr_t>(pool) % 16 || !table || !lens || !q || !out || !ws)
+    return JOLT_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % 16 || reinterpret_cast<uintptr_t>(ws) % 256) return JOLT_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_stride_b, q_stride_t) || (!k != !v) || (!prefix_out != !prefix_lse)) return JOLT_ERR_INVALID_ARG;
+  if (k && (!rows_ok(k, kv_stride_b, kv_stride_t) || !rows_ok(v, kv_stride_b, kv_stride_t))) return JOLT_ERR_INVALID_ARG;
+  const TreePlan t = tree_plan(*pages, batch, n_new, n_q, max_pages);
+  if (int64_t(pages->n_kv) * t.blocks > 65535) return JOLT_ERR_INVALID_ARG;
+  if (ws_bytes < t.ws_total) return JOLT_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  TreeArgs a{};
+  a.p = pages_dev(*pages, pool, table, max_pages, lens);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qsb = q_stride_b;
+  a.qst = q_stride_t;
+  a.ksb = kv_stride_b;
+  a.kst = kv_stride_t;
+  a.counts = counts;
+  a.mask = mask;
+  a.prefix_out = prefix_out;
+  a.prefix_lse = prefix_lse;
+  a.out = out;
+  a.lse = lse;
+  a.ml = reinterpret_cast<float2*>(w + sizeof(WsHeader));
+  a.acc = reinterpret_cast<float*>(w + t.ws_acc);
+  a.err = reinterpret_cast<int32_t*>(w);
+  a.scale2 = attn_scale * 1.4426950408889634f;
+  a.n_new = n_new;
+  a.n_q = n_q;
+  a.gq = n_q / pages->n_kv;
+  a.splits = t.splits;
+  a.parts = k ? t.parts : t.splits;
+  a.batch = batch;
+  a.blocks = t.blocks;
+  a.stages = t.stages;
+  a.stage_bytes = t.stage_bytes;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = pages->io_dtype == JOLT_F32;
+  if (pages->d_h == 128)
+    return f32 ? launch_tree_d<float, 128>(a, t, k != nullptr, st) : launch_tree_d<__nv_bfloat16, 128>(a, t, k != nullptr, st);
+  return f32 ? launch_tree_d<float, 64>(a, t, k != nullptr, st) : launch_tree_d<__nv_bfloat16, 64>(a, t, k != nullptr, st);
+}
