@@ -22,9 +22,14 @@ def _stream(stream=None):
     return C.c_void_p(0)
 
 
+def _device():
+    """The current device's index (initialises CUDA on first use)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
 def _raw(stream=None):
     """The stream as a plain integer (the current one by default)."""
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream
 
 
 def _ptr(t):
@@ -392,7 +397,7 @@ def _dev(t, dtype, shape, what, dev, inner=None):
     dimensions must be contiguous (None: all)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device.index != dev or t.device.type != "cuda":
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _bad(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, wanted {tuple(shape)} {dtype} on cuda:{dev}")
     if not t.is_contiguous():
         if inner is None:
@@ -412,7 +417,7 @@ def _steps(t, need):
 
 
 def _here(pages, pool, table, lens):
-    dev = torch.cuda.current_device()
+    dev = _device()
     if table.dim() != 2 or lens.dim() != 1 or pool.dim() != 1:
         _bad("pool [bytes], table [batch, max_pages] and lens [batch] are wanted")
     b, mp = table.shape
@@ -540,7 +545,7 @@ def rope(q, k, pos, inv_freq, q_out=None, k_out=None, layout="half", scaling=1.0
     q_out and k_out (default: new tensors; q_out may be q). pos int32 [n_tokens]; inv_freq fp32
     [rot_dim / 2]: the first rot_dim elements of each head are rotated. inverse: the transpose, the
     gradient of the forward call. Returns (q_out, k_out)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     one = q if q is not None else k
     if one is None or pos.dim() != 1 or inv_freq.dim() != 1 or one.dim() != 3 or layout not in ROPE_LAYOUTS:
         _bad("q, k [n_tokens, heads, d_h], pos [n_tokens], inv_freq [rot_dim / 2] and a layout are wanted")

@@ -1,5 +1,8 @@
 // jolt_pages_append / jolt_pages_read: the tail cache's rows coded as they are written, and read back.
+#include <algorithm>
+
 #include "common.cuh"
+#include "pages_codes.cuh"
 #include "pages.cuh"
 
 namespace jolt {
@@ -8,123 +11,236 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// E elements of a row at lane*E, as floats.
-template <int E>
-__device__ __forceinline__ void load_row(const float* p, float (&v)[E]) {
-  if constexpr (E == 4) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-  } else {
-    const float2 f = *reinterpret_cast<const float2*>(p);
-    v[0] = f.x; v[1] = f.y;
-  }
+// Two fp32 values in one 64-bit register, added or multiplied in one instruction each (IEEE per half).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-template <int E>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&v)[E]) {
-  uint32_t w[E / 2];
-  if constexpr (E == 4) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    w[0] = r.x; w[1] = r.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+__device__ __forceinline__ float2 f2_get(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Both kernels hold a row of D elements in four lanes, eight rows a warp (or sixteen as MMA rows): lane
+// m = lane % 4 has the 8-element pieces j*4 + m, j < D/32, so a load or store of one piece a lane covers
+// 64 contiguous bytes (bf16) of each row.
+__device__ __forceinline__ int piece_at(int j, int m) { return (j * 4 + m) * 8; }
+
+// Signs of this lane's elements: bit 8*j + e set when element piece_at(j, m) + e is negated.
+template <int D>
+__device__ __forceinline__ uint32_t lane_signs(uint64_t seed, int lane) {
+  uint32_t mine = 0;
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int j = 0; j < D / 32; ++j) {
+    const uint32_t w = __ballot_sync(0xffffffffu, rot_sign(seed, 32 * j + lane) < 0.f);
+    mine |= ((w >> (8 * (lane & 3))) & 0xFFu) << (8 * j);
   }
-}
-template <int E>
-__device__ __forceinline__ void store_row(float* p, const float (&v)[E]) {
-  if constexpr (E == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-}
-template <int E>
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[E]) {
-  uint32_t w[E / 2];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(p) = w[0];
+  return mine;
 }
 
 struct AppendArgs {
   PagesDev p;
-  const void* k;
-  const void* v;
+  const void* x[2];
   const int32_t* counts;
   const int32_t* src;
-  int64_t stride_b, stride_t, rows;
+  int64_t stride_b, stride_t;
   int32_t* err;
   int n_new, n_src;
+  uint32_t rows;  // of K, and of V
 };
 
-// One warp a row: rotate, quantise, pack. The arithmetic is jolt_rotate_rows then
-// jolt_quantize_pack, operation by operation, so the codes are theirs bit for bit.
-template <typename T, int E>
+// Eight elements at p as floats.
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Packs this lane's codes and stores them: piece j is B bytes at (j*4 + m)*B of the row.
+template <int B, int J>
+__device__ __forceinline__ void store_codes(const uint32_t (&c)[8 * J], uint8_t* row, int m) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    uint32_t w[B == 8 ? 2 : 1];
+#pragma unroll
+    for (int i = 0; i < (B == 8 ? 2 : 1); ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int e = 0; e < (B == 8 ? 4 : 8); ++e) w[i] |= c[8 * j + 4 * i + e] << (e * B);
+    }
+    uint8_t* dst = row + (j * 4 + m) * B;
+    if constexpr (B == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else if constexpr (B == 4) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else *reinterpret_cast<uint16_t*>(dst) = uint16_t(w[0]);
+  }
+}
+
+// Rotate, quantise and pack rows as they are written. The arithmetic is jolt_rotate_rows then
+// jolt_quantize_pack, operation by operation (butterflies over strides 1, 2, .. D/2 in that order, the
+// same roundings), so the codes are theirs bit for bit. The quotient a / scale is taken as
+// a * fl(1 / scale): with both roundings it is within 1.5 * 2^-23 |q| of the exact quotient and the
+// rounded one within 2^-24 |q|, so for |q| < levels + 1/2 both round to the same whole number unless
+// the product lies within levels * 2^-20 of a half-integer; only then is the division done. The
+// product is first clipped to (-1/2, levels + 1/2), where clipping and rounding commute.
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) k_append(const AppendArgs a) {
-  constexpr int D = 32 * E;
-  const int lane = threadIdx.x & 31;
+  constexpr int J = D / 32, N = 8 * J;  // pieces and elements of a lane
+  const int lane = threadIdx.x & 31, g = lane >> 2, m = lane & 3;
+  const int kv = blockIdx.y;
   const float isd = rsqrtf(float(D));
-  float sign[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) sign[i] = rot_sign(a.p.seed, lane * E + i);
-  const int64_t warps = int64_t(gridDim.x) * kWarps;
-  for (int64_t r = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < a.rows; r += warps) {
-    const int kv = int(r & 1);
-    const int64_t r2 = r >> 1;
-    const int h = int(r2 % a.p.n_kv);
-    const int64_t bi = r2 / a.p.n_kv;
-    const int i = int(bi % a.n_new), b = int(bi / a.n_new);
-    if (a.counts && i >= a.counts[b]) continue;
-    const int from = a.src ? a.src[int64_t(b) * a.n_new + i] : i;
-    const int at = pages_len(a.p, b, a.err) + i;
-    if (from < 0 || from >= a.n_src || at >= (a.p.max_pages << a.p.ps_log2)) {
-      report_error(a.err, JOLT_ERR_INVALID_ARG);
-      continue;
+  const uint32_t neg = lane_signs<D>(a.p.seed, lane);
+  const int bits = kv ? a.p.bv : a.p.bk;
+  const float levels = float((1 << bits) - 1);
+  const uint32_t step = gridDim.x * kWarps * 8;
+  for (uint32_t base = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * 8; base < a.rows; base += step) {
+    const uint32_t r = base + g;
+    // where the row comes from and goes to; a row that is not written runs along on zeros
+    const T* x = nullptr;
+    uint8_t* page_base = nullptr;
+    int row = 0;
+    if (r < a.rows) {
+      const uint32_t bi = r / uint32_t(a.p.n_kv), b = bi / uint32_t(a.n_new);
+      const int h = int(r - bi * a.p.n_kv), i = int(bi - b * a.n_new);
+      if (!a.counts || i < a.counts[b]) {
+        const int from = a.src ? a.src[int64_t(b) * a.n_new + i] : i;
+        const int at = pages_len(a.p, b, a.err) + i;
+        if (from < 0 || from >= a.n_src || at >= (a.p.max_pages << a.p.ps_log2)) {
+          report_error(a.err, JOLT_ERR_INVALID_ARG);
+        } else {
+          const int page = page_of(a.p, b, at, a.err);
+          if (page >= 0) {
+            page_base = a.p.pool + uint64_t(page) * a.p.page_bytes;
+            row = (h << a.p.ps_log2) + (at & ((1 << a.p.ps_log2) - 1));
+            x = static_cast<const T*>(a.x[kv]) + int64_t(b) * a.stride_b + int64_t(from) * a.stride_t + int64_t(h) * D;
+          }
+        }
+      }
     }
-    const int page = page_of(a.p, b, at, a.err);
-    if (page < 0) continue;
-    const T* x = static_cast<const T*>(kv ? a.v : a.k) + int64_t(b) * a.stride_b + int64_t(from) * a.stride_t +
-                 int64_t(h) * D + lane * E;
-    float v[E];
-    load_row<E>(x, v);
+    float v[N];
 #pragma unroll
-    for (int j = 0; j < E; ++j) v[j] *= sign[j];
-    warp_fwht<E>(v);
-    float bad = 0.f;
+    for (int j = 0; j < J; ++j) {
+      if (x) {
+        load8(x + piece_at(j, m), v + 8 * j);
+      } else {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      v[j] *= isd;
-      bad += v[j] * 0.f;
+        for (int e = 0; e < 8; ++e) v[8 * j + e] = 0.f;
+      }
     }
-    const int bits = kv ? a.p.bv : a.p.bk;
-    uint8_t c[E];
-    __half hs, hz;
-    const bool ok = warp_quantize<E>(v, bits, c, &hs, &hz) && bad == 0.f;
-    if (!ok) report_error(a.err, JOLT_ERR_NUMERIC);
-    uint32_t packed = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) packed |= uint32_t(c[j]) << (j * bits);
-    uint8_t* base = a.p.pool + uint64_t(page) * a.p.page_bytes;
-    const int row = (h << a.p.ps_log2) + (at & ((1 << a.p.ps_log2) - 1));
-    uint8_t* dst = base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
-    const int mine = E * bits;  // bits of this lane
-    if (mine == 32) {
-      reinterpret_cast<uint32_t*>(dst)[lane] = packed;
-    } else if (mine == 16) {
-      reinterpret_cast<uint16_t*>(dst)[lane] = uint16_t(packed);
-    } else if (mine == 8) {
-      dst[lane] = uint8_t(packed);
-    } else {
-      const uint32_t next = __shfl_down_sync(0xffffffffu, packed, 1);
-      if (!(lane & 1)) dst[lane >> 1] = uint8_t(packed | (next << 4));
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) ^ ((neg << (31 - i)) & 0x80000000u));
+    // stride 1 inside the packed pairs, then 2 and 4 on pairs
+    f2 y[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) y[i] = f2_make(v[2 * i] + v[2 * i + 1], v[2 * i] - v[2 * i + 1]);
+    const f2 minus = f2_make(-1.f, -1.f);
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (!(i & s)) {
+          const f2 p = y[i], q = y[i + s];
+          y[i] = f2_add(p, q);
+          y[i + s] = f2_fma(q, minus, p);
+        }
+    // strides 8 and 16 between lanes: p + q in the lower, p - q in the upper
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+      const float f = (m & s) ? -1.f : 1.f;
+      const f2 ff = f2_make(f, f);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 o = f2_get(y[i]);
+        const f2 other = f2_make(__shfl_xor_sync(0xffffffffu, o.x, s), __shfl_xor_sync(0xffffffffu, o.y, s));
+        y[i] = f2_fma(y[i], ff, other);
+      }
     }
-    if (lane == 0)
-      reinterpret_cast<__half2*>(base + (kv ? a.p.vs : a.p.ks))[row] = __halves2half2(hs, hz);
+    // strides 32 and 64 between pieces
+#pragma unroll
+    for (int s = 4; s < N / 2; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (!(i & s)) {
+          const f2 p = y[i], q = y[i + s];
+          y[i] = f2_add(p, q);
+          y[i + s] = f2_fma(q, minus, p);
+        }
+    const f2 isd2 = f2_make(isd, isd);
+    float lo = INFINITY, hi = -INFINITY, bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      y[i] = f2_mul(y[i], isd2);
+      const float2 t = f2_get(y[i]);
+      lo = fminf(lo, fminf(t.x, t.y));
+      hi = fmaxf(hi, fmaxf(t.x, t.y));
+      bad = fmaf(t.x, 0.f, fmaf(t.y, 0.f, bad));
+    }
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+    }
+    const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), levels)), hz = __float2half_rn(lo);
+    const float sc = __half2float(hs), zero = __half2float(hz);
+    const float rs = sc != 0.f ? __frcp_rn(sc) : 0.f;
+    const f2 mz = f2_make(-zero, -zero), rs2 = f2_make(rs, rs);
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+    const float top = levels + 0.4375f, margin = 0.5f - levels * 9.5367431640625e-7f;
+    uint32_t c[N], ties = 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 q = f2_get(f2_mul(f2_add(y[i], mz), rs2));
+      const float q0 = fminf(fmaxf(q.x, -0.4375f), top), q1 = fminf(fmaxf(q.y, -0.4375f), top);
+      const float r0 = q0 + kMagic, r1 = q1 + kMagic;
+      c[2 * i] = __float_as_uint(r0) & 0xFFu;
+      c[2 * i + 1] = __float_as_uint(r1) & 0xFFu;
+      if (fabsf(q0 - (r0 - kMagic)) >= margin) ties |= 1u << (2 * i);
+      if (fabsf(q1 - (r1 - kMagic)) >= margin) ties |= 1u << (2 * i + 1);
+    }
+    if (ties) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((ties >> i) & 1) {
+          const float2 t = f2_get(y[i >> 1]);
+          const float q = rintf(__fdiv_rn(__fsub_rn((i & 1) ? t.y : t.x, zero), sc));
+          c[i] = uint32_t(fminf(fmaxf(q, 0.f), levels));
+        }
+    }
+    const bool numeric = !(bad == 0.f) || !(fabsf(sc) < INFINITY) || !(fabsf(zero) < INFINITY);
+    if (page_base) {
+      uint8_t* dst = page_base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
+      if (bits == 4) store_codes<4, J>(c, dst, m);
+      else if (bits == 8) store_codes<8, J>(c, dst, m);
+      else store_codes<2, J>(c, dst, m);
+      if (m == 0) reinterpret_cast<__half2*>(page_base + (kv ? a.p.vs : a.p.ks))[row] = __halves2half2(hs, hz);
+      if (numeric) report_error(a.err, JOLT_ERR_NUMERIC);
+    }
   }
 }
 
@@ -132,69 +248,163 @@ struct ReadArgs {
   PagesDev p;
   void* out[2];
   const int32_t* start;
-  int64_t stride_b, stride_h, rows;
+  int64_t stride_b, stride_h;
   int32_t* err;
   int n_out;
 };
 
-// One warp a row: unpack, dequantise, rotate back.
-template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) k_read(const ReadArgs a) {
-  constexpr int D = 32 * E;
-  const int lane = threadIdx.x & 31;
-  const float isd = rsqrtf(float(D));
-  float back[E];
+// Words of this lane's pieces of a row, as code_pair takes them. Two bits: pieces 2i and 2i+1 share word i.
+template <int B, int J>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int m, uint32_t (&w)[J * B / 4]) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) back[i] = isd * rot_sign(a.p.seed, lane * E + i);
-  const int64_t warps = int64_t(gridDim.x) * kWarps;
-  for (int64_t r = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < a.rows; r += warps) {
-    const int i = int(r % a.n_out);
-    const int64_t r2 = r / a.n_out;
-    const int kv = int(r2 & 1);
-    const int h = int((r2 >> 1) % a.p.n_kv), b = int((r2 >> 1) / a.p.n_kv);
-    T* out = static_cast<T*>(a.out[kv]);
-    if (!out) continue;
-    const int from = a.start ? a.start[b] : 0;
-    if (from < 0) {
-      report_error(a.err, JOLT_ERR_INVALID_ARG);
-      continue;
+  for (int j = 0; j < J; ++j) {
+    const uint8_t* src = row + (j * 4 + m) * B;
+    if constexpr (B == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(src);
+      w[2 * j] = v.x;
+      w[2 * j + 1] = v.y;
+    } else if constexpr (B == 4) {
+      w[j] = *reinterpret_cast<const uint32_t*>(src);
+    } else {
+      const uint32_t v = *reinterpret_cast<const uint16_t*>(src);
+      w[j / 2] = (j & 1) ? (w[j / 2] | (v << 16)) : v;
     }
-    const int len = pages_len(a.p, b, a.err);
-    if (from >= len || i >= len - from) continue;
-    const int at = from + i;
-    const int page = page_of(a.p, b, at, a.err);
-    if (page < 0) continue;
-    const int bits = kv ? a.p.bv : a.p.bk;
-    const uint8_t* base = a.p.pool + uint64_t(page) * a.p.page_bytes;
-    const int row = (h << a.p.ps_log2) + (at & ((1 << a.p.ps_log2) - 1));
-    const uint8_t* codes = base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
-    const int mine = E * bits;
-    uint32_t packed;
-    if (mine == 32) packed = reinterpret_cast<const uint32_t*>(codes)[lane];
-    else if (mine == 16) packed = reinterpret_cast<const uint16_t*>(codes)[lane];
-    else if (mine == 8) packed = codes[lane];
-    else packed = codes[lane >> 1] >> ((lane & 1) * 4);
-    const __half2 sz = reinterpret_cast<const __half2*>(base + (kv ? a.p.vs : a.p.ks))[row];
-    const float s = __low2float(sz), z = __high2float(sz);
-    float v[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] = dequant((packed >> (j * bits)) & ((1u << bits) - 1u), s, z);
-    warp_fwht<E>(v);
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] *= back[j];
-    store_row<E>(out + int64_t(b) * a.stride_b + int64_t(h) * a.stride_h + int64_t(i) * D + lane * E, v);
   }
 }
 
-unsigned grid_for(int64_t rows) {
-  const int64_t g = (rows + kWarps - 1) / kWarps;
-  return unsigned(g < 148 * 8 ? g : 148 * 8);
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <>
+__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sixteen rows (16 aligned tokens of one head, so of one page) a warp. With the codes centred,
+//   H (scale c + zero) = scale (H c') + (D (zero + o scale)) e_0,   o = 2^(b-1),
+// so the Hadamard transform runs on whole numbers, exactly: four of the feature index's bits (those of
+// a pair's place among the k-slots of one m16n8k16 step) by MMAs with a matrix of signs, the others (the
+// step's) by butterflies of the accumulators. One rounding for scale / sqrt(D), one product, one
+// rounding to the output's type.
+template <typename T, int D, int B>
+__device__ __forceinline__ void read_tile(const uint8_t* codes, const __half2* szs, int g, int m, float isd, uint32_t neg,
+                                          T* out, int64_t first, int lo, int hi) {
+  constexpr int J = D / 32, NS = D / 16, W = J * B / 4;
+  uint32_t w[2][W];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) load_codes<B, J>(codes + (g + 8 * r) * (D * B / 8), m, w[r]);
+  // sign matrix: rows k = (lane m, register x, half hi), columns n = nt*8 + (m' * 2 + c): the output
+  // bit of m is m', that of x is c, that of hi is nt
+  const int mm = (g >> 1) & 3, c = g & 1;
+  const uint32_t s0 = (__popc(m & mm) & 1) ? 0xBC00BC00u : 0x3C003C00u;  // (-1, -1) or (1, 1)
+  const uint32_t s1 = c ? s0 ^ 0x80008000u : s0;
+  f2 acc[NS][2][2];
+#pragma unroll
+  for (int st = 0; st < NS; ++st) {
+    uint32_t a[4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      a[2 * x] = code_pair<B, W>(w[0], 2 * st + x);
+      a[2 * x + 1] = code_pair<B, W>(w[1], 2 * st + x);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t flip = nt ? 0x80000000u : 0u;
+      mma_f16_16816(d, a, s0 ^ flip, s1 ^ flip);
+      acc[st][nt][0] = f2_make(d[0], d[1]);
+      acc[st][nt][1] = f2_make(d[2], d[3]);
+    }
+  }
+  const f2 minus = f2_make(-1.f, -1.f);
+#pragma unroll
+  for (int s = 1; s < NS; s <<= 1)
+#pragma unroll
+    for (int st = 0; st < NS; ++st)
+      if (!(st & s)) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const f2 p = acc[st][nt][r], q = acc[st + s][nt][r];
+            acc[st][nt][r] = f2_add(p, q);
+            acc[st + s][nt][r] = f2_fma(q, minus, p);
+          }
+      }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int t = g + 8 * r;
+    if (t < lo || t >= hi) continue;
+    const float2 sz = __half22float2(szs[t]);
+    const float f = sz.x * isd;
+    const f2 ff = f2_make(f, f);
+    const float z0 = m == 0 ? (sz.y + float(1 << (B - 1)) * sz.x) * (isd * float(D)) : 0.f;
+    T* dst = out + (first + t) * D;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        // where the transform left element (j, e): see code_pair's order of a word's codes
+        const int st = B == 2 ? (j >> 1) * 4 + (e >> 1) : B == 4 ? 2 * j + ((e >> 1) & 1) : 2 * j + (e >> 2);
+        const int nt = B == 2 ? j & 1 : B == 4 ? e >> 2 : (e >> 1) & 1;
+        float2 x = f2_get(f2_mul(acc[st][nt][r], ff));
+        if (j == 0 && e == 0) x.x += z0;
+        v[e] = __uint_as_float(__float_as_uint(x.x) ^ ((neg << (31 - 8 * j - e)) & 0x80000000u));
+        v[e + 1] = __uint_as_float(__float_as_uint(x.y) ^ ((neg << (30 - 8 * j - e)) & 0x80000000u));
+      }
+      store8<T>(dst + piece_at(j, m), v);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) k_read(const ReadArgs a) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, m = lane & 3;
+  const int kv = blockIdx.y >= a.p.n_kv, h = blockIdx.y - kv * a.p.n_kv, b = blockIdx.z;
+  T* out = static_cast<T*>(a.out[kv]);
+  if (!out) return;
+  const int from = a.start ? a.start[b] : 0;
+  if (from < 0) {
+    report_error(a.err, JOLT_ERR_INVALID_ARG);
+    return;
+  }
+  const int len = pages_len(a.p, b, a.err);
+  const int end = min(len, from > len ? len : from + min(a.n_out, len - from));
+  if (from >= end) return;
+  out += int64_t(b) * a.stride_b + int64_t(h) * a.stride_h;
+  const uint32_t neg = lane_signs<D>(a.p.seed, lane);
+  const float isd = rsqrtf(float(D));
+  const int bits = kv ? a.p.bv : a.p.bk;
+  for (int t = (from >> 4) + blockIdx.x * kWarps + (threadIdx.x >> 5); t * 16 < end; t += gridDim.x * kWarps) {
+    const int page = page_of(a.p, b, t * 16, a.err);
+    if (page < 0) continue;
+    const uint8_t* base = a.p.pool + uint64_t(page) * a.p.page_bytes;
+    const int row = (h << a.p.ps_log2) + ((t * 16) & ((1 << a.p.ps_log2) - 1));
+    const uint8_t* codes = base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
+    const __half2* szs = reinterpret_cast<const __half2*>(base + (kv ? a.p.vs : a.p.ks)) + row;
+    const int64_t first = int64_t(t) * 16 - from;
+    const int lo = from - t * 16, hi = end - t * 16;  // rows of the tile that are wanted
+    if (bits == 4) read_tile<T, D, 4>(codes, szs, g, m, isd, neg, out, first, lo, hi);
+    else if (bits == 8) read_tile<T, D, 8>(codes, szs, g, m, isd, neg, out, first, lo, hi);
+    else read_tile<T, D, 2>(codes, szs, g, m, isd, neg, out, first, lo, hi);
+  }
 }
 
 // Checks shared by the calls over a pool.
 bool pool_args_ok(const jolt_pages* p, const void* pool, const int32_t* table, int32_t max_pages,
                   const int32_t* lens, int32_t batch) {
-  if (!pages_ok(p) || max_pages < 1 || batch < 0) return false;
+  if (!pages_ok(p) || max_pages < 1 || batch < 0 || batch > 65535) return false;
   if (int64_t(max_pages) * p->page_size > (int64_t(1) << 24)) return false;
   if (batch == 0) return true;
   return pool && table && lens && reinterpret_cast<uintptr_t>(pool) % 16 == 0;
@@ -217,27 +427,29 @@ extern "C" jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, co
   if (batch == 0 || n_new == 0) return JOLT_OK;
   if (!k || !v || (!src && n_new > n_src) || !rows_ok(k, stride_b, stride_t) || !rows_ok(v, stride_b, stride_t))
     return JOLT_ERR_INVALID_ARG;
+  const int64_t rows = int64_t(batch) * n_new * pages->n_kv;
+  if (rows >= int64_t(1) << 31) return JOLT_ERR_INVALID_ARG;
   AppendArgs a{};
   a.p = pages_dev(*pages, pool, table, max_pages, lens);
-  a.k = k;
-  a.v = v;
+  a.x[0] = k;
+  a.x[1] = v;
   a.counts = counts;
   a.src = src;
   a.stride_b = stride_b;
   a.stride_t = stride_t;
-  a.rows = int64_t(batch) * n_new * pages->n_kv * 2;
+  a.rows = uint32_t(rows);
   a.err = err;
   a.n_new = n_new;
   a.n_src = n_src;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = grid_for(a.rows);
+  const dim3 grid(unsigned(std::min<int64_t>((rows + kWarps * 8 - 1) / (kWarps * 8), 148 * 2)), 2);
   const bool f32 = pages->io_dtype == JOLT_F32;
   if (pages->d_h == 128) {
-    if (f32) k_append<float, 4><<<grid, kThreads, 0, st>>>(a);
-    else k_append<__nv_bfloat16, 4><<<grid, kThreads, 0, st>>>(a);
+    if (f32) k_append<float, 128><<<grid, kThreads, 0, st>>>(a);
+    else k_append<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(a);
   } else {
-    if (f32) k_append<float, 2><<<grid, kThreads, 0, st>>>(a);
-    else k_append<__nv_bfloat16, 2><<<grid, kThreads, 0, st>>>(a);
+    if (f32) k_append<float, 64><<<grid, kThreads, 0, st>>>(a);
+    else k_append<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(a);
   }
   JOLT_CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
@@ -258,18 +470,20 @@ extern "C" jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool
   a.start = start;
   a.stride_b = stride_b;
   a.stride_h = stride_h;
-  a.rows = int64_t(batch) * pages->n_kv * 2 * n_out;
   a.err = err;
   a.n_out = n_out;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = grid_for(a.rows);
+  // tiles of 16 aligned tokens that n_out rows can touch, and warps for them until the GPU is full
+  const int64_t tiles = (int64_t(n_out) + 30) / 16, lines = int64_t(batch) * pages->n_kv * 2;
+  const int64_t most = std::max<int64_t>(1, (148 * 8 + lines - 1) / lines);
+  const dim3 grid(unsigned(std::min((tiles + kWarps - 1) / kWarps, most)), 2 * pages->n_kv, batch);
   const bool f32 = pages->io_dtype == JOLT_F32;
   if (pages->d_h == 128) {
-    if (f32) k_read<float, 4><<<grid, kThreads, 0, st>>>(a);
-    else k_read<__nv_bfloat16, 4><<<grid, kThreads, 0, st>>>(a);
+    if (f32) k_read<float, 128><<<grid, kThreads, 0, st>>>(a);
+    else k_read<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(a);
   } else {
-    if (f32) k_read<float, 2><<<grid, kThreads, 0, st>>>(a);
-    else k_read<__nv_bfloat16, 2><<<grid, kThreads, 0, st>>>(a);
+    if (f32) k_read<float, 64><<<grid, kThreads, 0, st>>>(a);
+    else k_read<__nv_bfloat16, 64><<<grid, kThreads, 0, st>>>(a);
   }
   JOLT_CUDA_TRY(cudaGetLastError());
   return JOLT_OK;

@@ -74,9 +74,11 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::N]) {
 }
 
 // One pass over q and k: a block takes tb tokens, forms their table once for all heads, and each
-// thread turns 16-byte pieces: half layout, a piece of each half (two loads, two stores);
-// interleaved, one piece of whole pairs. Pieces past rot_dim are copied. x and y may be the same
-// memory: every piece is read and written by one thread.
+// thread turns 16-byte pieces of one place in the head, kRows rows (token, head) at a time with all
+// their loads in flight: half layout, a piece of each half; interleaved, one piece of whole pairs.
+// Pieces past rot_dim are copied. x and y may be the same memory: every piece is read and written by
+// one thread.
+constexpr int kRows = 4;
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
   constexpr int V = Vec<T>::N;
@@ -86,48 +88,60 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
   rope_table(a, t0, nt, cs);
   const int half = a.rot >> 1;
   const int rot_units = HALF ? half / V : a.rot / V;
-  const int units = rot_units + (a.d - a.rot) / V;  // per head
+  const int units = rot_units + (a.d - a.rot) / V;  // pieces of a head, at most 128
   const int heads = a.t[0].heads + a.t[1].heads;
-  const int total = nt * heads * units;
-  for (int i = threadIdx.x; i < total; i += kThreads) {
-    const int row = i / units, u = i - row * units;
-    const int t = row / heads;
-    int h = row - t * heads;
-    const int which = h >= a.t[0].heads;
-    const RopeTensor& x = a.t[which];
-    if (which) h -= a.t[0].heads;
-    const T* src = static_cast<const T*>(x.x) + (t0 + t) * x.sx + int64_t(h) * a.d;
-    T* dst = static_cast<T*>(x.y) + (t0 + t) * x.sy + int64_t(h) * a.d;
-    if (u >= rot_units) {
-      const int at = a.rot + (u - rot_units) * V;
-      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
-      continue;
+  const int u = threadIdx.x % units, at_once = kThreads / units;
+  if (int(threadIdx.x) >= at_once * units) return;
+  const bool turn = u < rot_units;
+  const int at = turn ? u * V : a.rot + (u - rot_units) * V;
+  const int rows = nt * heads;
+  for (int r0 = threadIdx.x / units; r0 < rows; r0 += kRows * at_once) {
+    uint4 pa[kRows], pb[kRows];
+    T* dst[kRows];
+    int tok[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int row = r0 + i * at_once;
+      if (row >= rows) break;
+      tok[i] = row / heads;
+      int h = row - tok[i] * heads;
+      const int which = h >= a.t[0].heads;
+      const RopeTensor& x = a.t[which];
+      if (which) h -= a.t[0].heads;
+      const T* src = static_cast<const T*>(x.x) + (t0 + tok[i]) * x.sx + int64_t(h) * a.d + at;
+      dst[i] = static_cast<T*>(x.y) + (t0 + tok[i]) * x.sy + int64_t(h) * a.d + at;
+      pa[i] = *reinterpret_cast<const uint4*>(src);
+      if (HALF && turn) pb[i] = *reinterpret_cast<const uint4*>(src + half);
     }
-    const float2* c = cs + t * half;
-    if (HALF) {
-      const uint4 ra = *reinterpret_cast<const uint4*>(src + u * V);
-      const uint4 rb = *reinterpret_cast<const uint4*>(src + half + u * V);
-      float p[V], q[V], y[V], z[V];
-      unpack<T>(ra, p);
-      unpack<T>(rb, q);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 f = c[u * V + j];
-        y[j] = p[j] * f.x - q[j] * f.y;
-        z[j] = q[j] * f.x + p[j] * f.y;
+    for (int i = 0; i < kRows; ++i) {
+      if (r0 + i * at_once >= rows) break;
+      if (!turn) {
+        *reinterpret_cast<uint4*>(dst[i]) = pa[i];
+        continue;
       }
-      *reinterpret_cast<uint4*>(dst + u * V) = pack<T>(y);
-      *reinterpret_cast<uint4*>(dst + half + u * V) = pack<T>(z);
-    } else {
+      const float2* c = cs + tok[i] * half;
       float p[V], y[V];
-      unpack<T>(*reinterpret_cast<const uint4*>(src + u * V), p);
+      unpack<T>(pa[i], p);
+      if (HALF) {
+        float q[V], z[V];
+        unpack<T>(pb[i], q);
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float2 f = c[u * (V / 2) + j];
-        y[2 * j] = p[2 * j] * f.x - p[2 * j + 1] * f.y;
-        y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
+        for (int j = 0; j < V; ++j) {
+          const float2 f = c[u * V + j];
+          y[j] = p[j] * f.x - q[j] * f.y;
+          z[j] = q[j] * f.x + p[j] * f.y;
+        }
+        *reinterpret_cast<uint4*>(dst[i] + half) = pack<T>(z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float2 f = c[u * (V / 2) + j];
+          y[2 * j] = p[2 * j] * f.x - p[2 * j + 1] * f.y;
+          y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
+        }
       }
-      *reinterpret_cast<uint4*>(dst + u * V) = pack<T>(y);
+      *reinterpret_cast<uint4*>(dst[i]) = pack<T>(y);
     }
   }
 }
@@ -219,7 +233,8 @@ extern "C" jolt_status jolt_rope(const void* q, void* q_out, int32_t n_q, int64_
   a.d = d_h;
   a.rot = rot_dim;
   a.inverse = inverse;
-  a.tb = 1;
+  // several tokens a block once there are blocks enough for every SM
+  a.tb = int(std::min<int64_t>(4, std::max<int64_t>(1, n_tokens / (148 * 8))));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return io_dtype == JOLT_F32 ? launch_rope<float>(a, layout == JOLT_ROPE_HALF, vec, st)
                               : launch_rope<__nv_bfloat16>(a, layout == JOLT_ROPE_HALF, vec, st);

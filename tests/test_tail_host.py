@@ -154,3 +154,24 @@ def test_attention_refusals():
     assert need > 256 and call(wsb=need - 1) == -6
     for bad in ((-1, 2, 8, 4), (1, 65, 8, 4), (1, 2, 9, 4), (1, 2, 8, 0)):
         assert _lib.lib().jolt_tree_attn_workspace(C.byref(p), *bad) == 0
+
+
+def test_quotient_by_reciprocal_gives_the_divisions_codes():
+    """jolt_pages_append's quotient: clip(a fl(1/s)) rounded, the division only within levels * 2^-20 of a
+    half-integer, against clip(rint(a / s)), in float32, near-ties planted one and two ulps either side."""
+    f32, rng = np.float32, np.random.default_rng(12)
+    for levels in (3, 15, 255):
+        s = np.concatenate([rng.uniform(1e-4, 4.0, 300000), 2.0 ** rng.uniform(-24, 15, 100000)]).astype(np.float16)
+        s = s[s > 0].astype(f32)
+        k = rng.integers(-2, levels + 2, s.size).astype(f32)
+        tie = ((k + f32(0.5)) * s).astype(f32)
+        up, down = np.nextafter(tie, f32(np.inf)), np.nextafter(tie, f32(-np.inf))
+        some = (rng.uniform(-0.7, levels + 0.7, s.size).astype(f32) * s).astype(f32)
+        for a in (some, tie, up, down, np.nextafter(up, f32(np.inf)), np.nextafter(down, f32(-np.inf)), (some * f32(1e4)).astype(f32)):
+            q = np.clip((a * (f32(1) / s).astype(f32)).astype(f32), f32(-0.4375), f32(levels) + f32(0.4375))
+            c = np.rint(q)
+            near = np.abs((q - c).astype(f32)) >= f32(0.5) - f32(levels) * f32(2.0 ** -20)
+            want = np.clip(np.rint((a / s).astype(f32)), 0, levels)
+            got = np.where(near, want, c)
+            assert np.array_equal(np.abs(got), want)
+            assert near.mean() < 1e-3 or a is not some
