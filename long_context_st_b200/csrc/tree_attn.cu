@@ -17,7 +17,7 @@
 
 #include "pages_codes.cuh"
 #include "sm100.cuh"
-#include "pages.cuh"
+#include "tree_attn.cuh"
 
 namespace jolt {
 namespace {
@@ -26,42 +26,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // tokens a warp takes at a time
 constexpr int kMaxSplits = 63;   // + the drafted tokens' own partial: two per lane in the merge
-constexpr int kMaxDraft = 64;    // bits of a mask word
 constexpr int kMaxStages = 4;
-
-struct TreeArgs {
-  PagesDev p;
-  const void* q;
-  const void* k;
-  const void* v;
-  int64_t qsb, qst, ksb, kst;
-  const int32_t* counts;
-  const uint64_t* mask;
-  const void* prefix_out;
-  const float* prefix_lse;
-  void* out;
-  float* lse;
-  float2* ml;   // [rows][parts] (maximum in log2 units, sum)
-  float* acc;   // [rows][parts][D]
-  int32_t* err;
-  float scale2;  // attn_scale * log2(e): scores are kept in log2 units
-  int n_new, n_q, gq, splits, parts, batch, blocks, stages, stage_bytes;
-};
-
-__device__ __forceinline__ int draft_count(const TreeArgs& a, int b) {
-  return a.counts ? min(max(a.counts[b], 0), a.n_new) : a.n_new;
-}
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
-__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t h2_pack(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 h2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
 // Keys of one tile: acc[grp][nt] += codes (tokens grp*16 + {g, g+8}) x R q (columns of tile nt).
 template <int D, int B, int NT, int QT>
@@ -124,98 +89,6 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
   }
 }
 
-// The drafted tokens' own keys and values, in fp32 on the CUDA cores (at most 64 keys).
-template <typename T, int D, int RB>
-__device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* smem) {
-  constexpr int E = D / 32, KS = D + 4;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cnt = draft_count(a, b);
-  const int rows = min(RB, cnt * a.gq - r0);
-  if (rows <= 0) return;
-  float* ks = reinterpret_cast<float*>(smem);           // [cnt][KS]
-  float* vs = ks + kMaxDraft * KS;                      // [cnt][D]
-  float* qs = vs + kMaxDraft * D;                       // [RB][D]
-  float* ps = qs + RB * D;                              // [warp][4][64]
-  const T* kb = static_cast<const T*>(a.k) + int64_t(b) * a.ksb + int64_t(h) * D;
-  const T* vb = static_cast<const T*>(a.v) + int64_t(b) * a.ksb + int64_t(h) * D;
-  for (int i = tid; i < cnt * D; i += kThreads) {
-    const int t = i / D, f = i % D;
-    ks[t * KS + f] = ld_as_float(kb, t * a.kst + f);
-    vs[t * D + f] = ld_as_float(vb, t * a.kst + f);
-  }
-  const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
-  for (int i = tid; i < rows * D; i += kThreads) {
-    const int r = r0 + i / D, f = i % D;
-    qs[i] = ld_as_float(qb, int64_t(r / a.gq) * a.qst + (r % a.gq) * D + f) * a.scale2;
-  }
-  __syncthreads();
-  for (int q0 = warp * 4; q0 < rows; q0 += kWarps * 4) {
-    uint64_t bits[4];
-    float s[4][2];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = (r0 + q0 + r) / a.gq;
-      bits[r] = 0;
-      if (q0 + r < rows) bits[r] = a.mask ? a.mask[int64_t(b) * a.n_new + i] : ~uint64_t(0) >> (63 - i);
-      if (cnt < 64) bits[r] &= (uint64_t(1) << cnt) - 1;
-      s[r][0] = s[r][1] = 0.f;
-    }
-    const int j1 = min(lane, cnt - 1), j2 = min(lane + 32, cnt - 1);
-    for (int f = 0; f < D; f += 4) {
-      const float4 k1 = *reinterpret_cast<const float4*>(ks + j1 * KS + f);
-      const float4 k2 = *reinterpret_cast<const float4*>(ks + j2 * KS + f);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(qs + min(q0 + r, rows - 1) * D + f);
-        s[r][0] += x.x * k1.x + x.y * k1.y + x.z * k1.z + x.w * k1.w;
-        s[r][1] += x.x * k2.x + x.y * k2.y + x.z * k2.z + x.w * k2.w;
-      }
-    }
-    float o[4][E];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const bool v1 = (bits[r] >> lane) & 1, v2 = (bits[r] >> (lane + 32)) & 1;
-      const float s1 = v1 ? s[r][0] : -INFINITY, s2 = v2 ? s[r][1] : -INFINITY;
-      const float mx = warp_max(fmaxf(s1, s2));
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float p1 = v1 ? exp2f(s1 - ref) : 0.f, p2 = v2 ? exp2f(s2 - ref) : 0.f;
-      const float l = warp_sum(p1 + p2);
-      ps[(warp * 4 + r) * 64 + lane] = p1;
-      ps[(warp * 4 + r) * 64 + lane + 32] = p2;
-      if (lane == 0 && q0 + r < rows) {
-        const int row = r0 + q0 + r;
-        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
-        a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[r][e] = 0.f;
-    }
-    __syncwarp();
-    for (int j = 0; j < cnt; ++j) {
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = vs[j * D + lane * E + e];
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if ((bits[r] >> j) & 1) {  // a masked row of v is not touched: it may hold anything
-          const float p = ps[(warp * 4 + r) * 64 + j];
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[r][e] += p * v[e];
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (q0 + r < rows) {
-        const int row = r0 + q0 + r;
-        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
-        float* dst = a.acc + (gr * a.parts + a.splits) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dst[e] = o[r][e];
-      }
-    __syncwarp();
-  }
-}
-
 // Scores, online softmax and values of one split of a sequence's pages for one KV head and up to RB
 // query rows (drafted token x head of the group). The MMAs have tokens (keys) or features (values)
 // as their 16 rows and query rows as their 8 columns, so single-token decoding wastes little; with
@@ -235,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   const int h = blockIdx.y / a.blocks, r0 = (blockIdx.y % a.blocks) * RB, b = blockIdx.z;
   const int split = blockIdx.x;
   if (split == a.splits) {
-    draft_block<T, D, RB>(a, b, h, r0, smem);
+    draft_block<T, D, RB, kThreads>(a, b, h, r0, smem);
     return;
   }
   const int cnt = draft_count(a, b);
@@ -603,7 +476,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   const float* acc = a.acc + row * a.parts * D + lane * E;
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < a.cached; ++s) {
     const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
     if (f != 0.f) {
 #pragma unroll
@@ -614,10 +487,10 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] *= back[e];
   if (draft) {
-    const float f = __shfl_sync(0xffffffffu, a.splits < 32 ? w[0] : w[1], a.splits & 31);
+    const float f = __shfl_sync(0xffffffffu, a.cached < 32 ? w[0] : w[1], a.cached & 31);
     if (f != 0.f) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.splits) * D + e];
+      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.cached) * D + e];
     }
   }
   if (wp != 0.f) {
@@ -635,14 +508,23 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 // ---- host -------------------------------------------------------------------------------------------
 
 struct TreePlan {
-  int nt, blocks, splits, parts, stages, stage_bytes;
-  bool pack;
+  int nt, blocks, splits, cached, parts, stages, stage_bytes;
+  bool pack, tc;
   size_t smem, ws_acc, ws_total;
 };
 
 TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_pages) {
   TreePlan t{};
   const int rows = n_new * (n_q / p.n_kv);
+  if (rows > 32 && p.io_dtype == JOLT_BF16) {
+    t.tc = true;
+    t.blocks = (rows + 127) / 128;
+    const int64_t units = int64_t(batch) * p.n_kv * t.blocks;
+    const int64_t tiles = (int64_t(max_pages) * p.page_size + 127) / 128;
+    t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits / 2, (tiles + 1) / 2, 148 / units})));
+    t.cached = 2 * t.splits;
+    t.smem = tree_tc_smem(p.d_h);
+  } else {
   t.pack = rows <= 4;
   t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   t.blocks = (rows + 8 * t.nt - 1) / (8 * t.nt);
@@ -650,7 +532,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const int64_t tiles = (int64_t(max_pages) * p.page_size + kTile - 1) / kTile;
   const int resident = 148 * (t.nt == 1 ? 2 : 1);
   t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + kWarps - 1) / kWarps, resident / units})));
-  t.parts = t.splits + 1;
+  t.cached = t.splits;
   t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
   const int budget = (t.nt == 1 ? 100 : 190) * 1024;
   t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
@@ -660,6 +542,8 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
   const size_t draft = size_t(kMaxDraft) * (2 * p.d_h + 4) * 4 + size_t(t.pack ? 4 : C) * p.d_h * 4 + kWarps * 4 * 64 * 4;
   t.smem = std::max(head + std::max(ring, red), draft);
+  }
+  t.parts = t.cached + 1;
   const size_t nrows = size_t(batch) * n_new * n_q;
   t.ws_acc = align_up(sizeof(WsHeader) + nrows * t.parts * sizeof(float2), 256);
   t.ws_total = align_up(t.ws_acc + nrows * t.parts * p.d_h * sizeof(float), 256);
@@ -671,12 +555,8 @@ bool tree_dims_ok(const jolt_pages* p, int batch, int n_new, int n_q, int max_pa
          n_q % p->n_kv == 0 && n_q <= 65536 && max_pages >= 1 && int64_t(max_pages) * p->page_size <= (int64_t(1) << 24);
 }
 
-template <typename T, int D, int NT, bool PACK>
-jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
-  JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree<T, D, NT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(t.smem)));
-  const dim3 grid(t.splits + (draft ? 1 : 0), a.p.n_kv * t.blocks, a.batch);
-  k_tree<T, D, NT, PACK><<<grid, kThreads, t.smem, st>>>(a);
-  JOLT_CUDA_TRY(cudaGetLastError());
+template <typename T, int D>
+jolt_status launch_merge(const TreeArgs& a, bool draft, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((int64_t(a.batch) * a.n_new * a.n_q + 3) / 4));
   cfg.blockDim = dim3(128);
@@ -690,8 +570,21 @@ jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaSt
   return JOLT_OK;
 }
 
+template <typename T, int D, int NT, bool PACK>
+jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
+  JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree<T, D, NT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(t.smem)));
+  const dim3 grid(t.splits + (draft ? 1 : 0), a.p.n_kv * t.blocks, a.batch);
+  k_tree<T, D, NT, PACK><<<grid, kThreads, t.smem, st>>>(a);
+  JOLT_CUDA_TRY(cudaGetLastError());
+  return launch_merge<T, D>(a, draft, st);
+}
+
 template <typename T, int D>
 jolt_status launch_tree_d(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
+  if (t.tc) {
+    const jolt_status r = launch_tree_tc(a, D, draft, t.smem, st);
+    return r != JOLT_OK ? r : launch_merge<T, D>(a, draft, st);
+  }
   if (t.pack) return launch_tree<T, D, 1, true>(a, t, draft, st);
   if (t.nt == 1) return launch_tree<T, D, 1, false>(a, t, draft, st);
   if (t.nt == 2) return launch_tree<T, D, 2, false>(a, t, draft, st);
@@ -755,7 +648,8 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   a.n_q = n_q;
   a.gq = n_q / pages->n_kv;
   a.splits = t.splits;
-  a.parts = k ? t.parts : t.splits;
+  a.cached = t.cached;
+  a.parts = k ? t.parts : t.cached;
   a.batch = batch;
   a.blocks = t.blocks;
   a.stages = t.stages;

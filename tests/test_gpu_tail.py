@@ -411,6 +411,20 @@ def test_attention_scales_far_apart(cuda_ok):
         check_case(c)
 
 
+@pytest.mark.parametrize("d,n,nq", [(128, 40, 2), (64, 40, 2), (128, 2, 2), (64, 9, 2)])
+def test_attention_rising_scores(cuda_ok, d, n, nq):
+    """Key scales that grow along the sequence: a row's maximum is passed again and again, inside a tile too."""
+    c = attn_case(49, [900, 300], n, nq, 1, d, 4, 8, 16, "bf16")
+    p, pool, table = c[:3]
+    off, size = api.pages_layout(p)
+    pages, tab = pool.view(p.n_pages, size), table.cpu().numpy()
+    for b, length in enumerate(c[3]):
+        for i in range(-(-length // 16)):
+            sz = pages[tab[b, i], off[1]:off[1] + 16 * 4].view(torch.float16).view(16, 2)
+            sz.copy_((sz.float() * (0.02 * (i * 16 + torch.arange(16, device="cuda")[:, None]) + 0.1)).half())
+    check_case(c)
+
+
 # ---- streams, graphs, devices ------------------------------------------------------------------------
 
 def test_captured_calls_follow_lengths_and_positions(cuda_ok):
