@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   const int h = blockIdx.y / a.blocks, r0 = (blockIdx.y % a.blocks) * RB, b = blockIdx.z;
   const int split = blockIdx.x;
   if (split == a.splits) {
-    draft_block<T, D, RB, kThreads>(a, b, h, r0, smem);
+    draft_part<T, D, RB, kThreads>(a, b, h, r0, smem);
     return;
   }
   const int cnt = draft_count(a, b);
@@ -540,7 +540,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 8 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
   const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
   const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
-  const size_t draft = size_t(kMaxDraft) * (2 * p.d_h + 4) * 4 + size_t(t.pack ? 4 : C) * p.d_h * 4 + kWarps * 4 * 64 * 4;
+  const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
   t.smem = std::max(head + std::max(ring, red), draft);
   }
   t.parts = t.cached + 1;

@@ -27,6 +27,13 @@ struct TreeArgs {
   int cached;  // partial results of the pages (splits, or two a split); the drafted tokens' follows them
 };
 
+// Shared memory of the drafted tokens' part for blocks of `rows` query rows.
+inline size_t draft_smem(int d_h, int rows, int threads) {
+  const size_t cores = size_t(kMaxDraft) * (2 * d_h + 4) * 4 + size_t(rows) * d_h * 4 + size_t(threads / 32) * 4 * 64 * 4;
+  const size_t mma = size_t(2 * kMaxDraft + (rows + 15) / 16 * 16) * (d_h + 8) * 2 + 8;
+  return cores > mma ? cores : mma;
+}
+
 #if defined(__CUDACC__)
 __device__ __forceinline__ int draft_count(const TreeArgs& a, int b) {
   return a.counts ? min(max(a.counts[b], 0), a.n_new) : a.n_new;
@@ -135,6 +142,182 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
   }
 }
 
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+}
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf2_pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The same for bf16 on m16n8k16 MMAs, 16 query rows a warp: q, k and v are bf16 as given, so the scores are
+// exact products; p goes in as two bf16 terms (16 bits). A row that masks a token multiplies its values by 0,
+// so values that are not finite are taken as 0 in the MMAs and added to the rows that see them.
+template <int D, int RB, int THREADS>
+__device__ void draft_mma(const TreeArgs& a, int b, int h, int r0, uint8_t* smem) {
+  constexpr int LD = D + 8, RT = (RB + 15) / 16, V = D / 8;  // padded row; row tiles; 16-byte pieces of a row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, m = lane & 3;
+  const int cnt = draft_count(a, b), keys = (cnt + 15) / 16 * 16;
+  const int rows = min(RB, cnt * a.gq - r0);
+  __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(smem);  // [64][LD]
+  __nv_bfloat16* vs = ks + kMaxDraft * LD;                     // [64][LD]
+  __nv_bfloat16* qs = vs + kMaxDraft * LD;                     // [RT * 16][LD]
+  const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(a.k) + int64_t(b) * a.ksb + int64_t(h) * D;
+  const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(a.v) + int64_t(b) * a.ksb + int64_t(h) * D;
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
+  unsigned long long* bad = reinterpret_cast<unsigned long long*>(qs + RT * 16 * LD);  // tokens with such values
+  if (tid == 0) *bad = 0;
+  __syncthreads();
+  for (int i = tid; i < keys * V; i += THREADS) {
+    const int t = i / V, f = (i % V) * 8;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (t < cnt) {
+      x = *reinterpret_cast<const uint4*>(kb + t * a.kst + f);
+      y = *reinterpret_cast<const uint4*>(vb + t * a.kst + f);
+    }
+    *reinterpret_cast<uint4*>(ks + t * LD + f) = x;
+    uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7F80u) == 0x7F80u) odd = true, w[e] &= 0xFFFF0000u;
+      if ((w[e] & 0x7F800000u) == 0x7F800000u) odd = true, w[e] &= 0xFFFFu;
+    }
+    if (odd) atomicOr(bad, 1ull << t);
+    *reinterpret_cast<uint4*>(vs + t * LD + f) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const int tiles = (rows + 15) / 16;
+  for (int i = tid; i < tiles * 16 * V; i += THREADS) {
+    const int r = i / V, f = (i % V) * 8, row = r0 + r;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows) x = *reinterpret_cast<const uint4*>(qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + f);
+    *reinterpret_cast<uint4*>(qs + r * LD + f) = x;
+  }
+  __syncthreads();
+  const uint64_t not_finite = *bad;
+  for (int rt = warp; rt < tiles; rt += THREADS / 32) {
+    float s[8][4];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+#pragma unroll 2
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t q[4];
+      ldsm4(q, qs + (rt * 16 + (lane & 15)) * LD + kk * 16 + (lane >> 4) * 8);
+#pragma unroll
+      for (int nt = 0; nt < 8; nt += 2)
+        if (nt * 8 < keys) {
+          uint32_t k[4];
+          ldsm4(k, ks + (nt * 8 + (lane & 7) + (lane >> 4) * 8) * LD + kk * 16 + ((lane >> 3) & 1) * 8);
+          mma_bf16_16816(s[nt], q, k[0], k[1]);
+          mma_bf16_16816(s[nt + 1], q, k[2], k[3]);
+        }
+    }
+    uint32_t ph[4][4], pl[4][4];
+    uint64_t extra[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {  // rows g and g + 8
+      const int r = rt * 16 + g + 8 * x, i = (r0 + r) / a.gq;
+      uint64_t bits = 0;
+      if (r < rows) bits = a.mask ? a.mask[int64_t(b) * a.n_new + i] : ~uint64_t(0) >> (63 - i);
+      if (cnt < 64) bits &= (uint64_t(1) << cnt) - 1;
+      extra[x] = bits & not_finite;
+      bits >>= 2 * m;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& v = s[nt][2 * x + c];
+          v = (bits >> (8 * nt + c)) & 1 ? v * a.scale2 : -INFINITY;
+          mx = fmaxf(mx, v);
+        }
+#pragma unroll
+      for (int y = 1; y <= 2; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float l = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        float p[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          p[c] = (bits >> (8 * nt + c)) & 1 ? exp2f(s[nt][2 * x + c] - ref) : 0.f;
+          l += p[c];
+        }
+        const uint32_t hi = bf2_pack(p[0], p[1]);
+        ph[nt >> 1][x + 2 * (nt & 1)] = hi;
+        pl[nt >> 1][x + 2 * (nt & 1)] = bf2_pack(p[0] - __uint_as_float(hi << 16), p[1] - __uint_as_float(hi & 0xFFFF0000u));
+      }
+#pragma unroll
+      for (int y = 1; y <= 2; y <<= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
+      if (r < rows && m == 0) {
+        const int64_t gr = (int64_t(b) * a.n_new + i) * a.n_q + h * a.gq + (r0 + r) % a.gq;
+        a.ml[gr * a.parts + a.cached] = make_float2(mx, l);
+      }
+    }
+    float* dst[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = rt * 16 + g + 8 * x, row = r0 + r;
+      dst[x] = r < rows ? a.acc + (((int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq) * a.parts + a.cached) * D
+                        : nullptr;
+    }
+#pragma unroll 2
+    for (int f = 0; f < D; f += 16) {
+      float o[2][4] = {};
+#pragma unroll
+      for (int kg = 0; kg < 4; ++kg)
+        if (kg * 16 < keys) {
+          uint32_t v[4];  // keys kg*16 .. + 15, features f .. + 15
+          ldsm4_trans(v, vs + (kg * 16 + (lane & 15)) * LD + f + (lane >> 4) * 8);
+          mma_bf16_16816(o[0], ph[kg], v[0], v[1]);
+          mma_bf16_16816(o[0], pl[kg], v[0], v[1]);
+          mma_bf16_16816(o[1], ph[kg], v[2], v[3]);
+          mma_bf16_16816(o[1], pl[kg], v[2], v[3]);
+        }
+      if (not_finite) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          for (uint64_t left = extra[x]; left; left &= left - 1) {
+            const __nv_bfloat16* v = vb + int64_t(__ffsll(left) - 1) * a.kst + f + 2 * m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = __bfloat162float(v[(e >> 1) * 8 + (e & 1)]);
+              if (!(fabsf(y) < INFINITY)) o[e >> 1][2 * x + (e & 1)] += y;
+            }
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (dst[x]) {
+          *reinterpret_cast<float2*>(dst[x] + f + 2 * m) = make_float2(o[0][2 * x], o[0][2 * x + 1]);
+          *reinterpret_cast<float2*>(dst[x] + f + 8 + 2 * m) = make_float2(o[1][2 * x], o[1][2 * x + 1]);
+        }
+    }
+  }
+}
+
+template <typename T, int D, int RB, int THREADS>
+__device__ __forceinline__ void draft_part(const TreeArgs& a, int b, int h, int r0, uint8_t* smem) {
+  if (draft_count(a, b) * a.gq <= r0) return;
+  if constexpr (sizeof(T) == 2) draft_mma<D, RB, THREADS>(a, b, h, r0, smem);
+  else draft_block<T, D, RB, THREADS>(a, b, h, r0, smem);
+}
 #endif
 
 // The form for bf16 and more than 32 query rows a KV head (tree_tc.cu).

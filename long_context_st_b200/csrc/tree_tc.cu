@@ -8,8 +8,8 @@
 //   S = (R q, two f16 terms) x codes^T    A, B from shared memory, K-major
 //   O += P x codes                        A = P (f16) in tensor memory over the scores it came from,
 //                                         B = codes from shared memory, token rows as they are (MN-major)
-// Warps: 0-3 and 4-7 softmax of the two streams, 8-11 widen the keys' codes (global -> registers -> f16
-// tiles in shared memory), 12-15 the values', 16 issues the MMAs. Both code tiles have one layout: a
+// Warps: 0-7 and 8-15 softmax of the two streams (16 rows each), 16-19 widen the keys' codes (global ->
+// registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs. Both code tiles have one layout: a
 // token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8. Features stand in
 // the order in which the widening leaves them; R q is laid out to match, and the outputs are put back
 // at the end.
@@ -26,14 +26,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 640;  // five warpgroups
+constexpr int kThreads = 896;  // seven warpgroups
 constexpr int kRows = 128;   // query rows of a block
 constexpr int kTok = 128;    // tokens of a tile
-// registers a thread after the warpgroups' re-split (launch: 96 each)
-constexpr int kRegLaunch = 96, kRegSoft = 152, kRegWiden = 64, kRegMma = 48;
-static_assert(2 * kRegSoft + 2 * kRegWiden + kRegMma <= 5 * kRegLaunch, "register shares");
-constexpr float kSlack = 8.f;  // log2 units a row's scores may pass its reference by: p <= 2^8
-constexpr int kPExp = 7;       // p * scale is carried times 2^(7 - ve): below 2^15
+// registers a thread after the warpgroups' re-split (launch: 72 each)
+constexpr int kRegLaunch = 72, kRegSoft = 80, kRegWiden = 64, kRegMma = 48;
+static_assert(4 * kRegSoft + 2 * kRegWiden + kRegMma <= 7 * kRegLaunch, "register shares");
+constexpr float kPExp = 7.f;     // p is carried times 2^7
+constexpr float kRoom = 4.f;     // how far above a row's maximum its reference is set
+constexpr float kMost = 32768.f;  // and a thread's sum of eight of them below 2^15, so that each is within f16
+// A value is taken from its code's bits as an f16 number c 2^-24 by one multiply-add, whose factor has to be
+// an f16 number too: values are carried times 2^(kVExp - ve), so that a scale of at most 2^(ve + 1 - b) gives
+// at most 2^15.5. They then reach 2^(b - 10), and besides f16's 2^-12 are off by at most 2^-25, 2^-(15 + b)
+// of the largest value met.
+template <int BV>
+constexpr int kVExp = BV - 10;
 
 template <int D>
 struct Smem {
@@ -42,9 +49,9 @@ struct Smem {
   static constexpr int q = 0;                      // two terms
   static constexpr int k = q + 2 * kTile;          // two buffers
   static constexpr int v = k + 2 * kTile;          // two buffers
-  static constexpr int sc = v + 2 * kTile;         // [2][64 token pairs][8] floats
-  static constexpr int rs = sc + 2 * 64 * 32;      // [128] 2^-k
-  static constexpr int qs = rs + 512;              // [128] 2^k sum(R q)
+  static constexpr int sc = v + 2 * kTile;         // [2][64 token pairs][4] floats: key scales, key zeros
+  static constexpr int rs = sc + 2 * 64 * 16;      // [28] warps' largest |R q|
+  static constexpr int qs = rs + 128;              // [128] sum(R q)
   static constexpr int vis = qs + 512;             // [2][4] words: visible tokens
   static constexpr int ve = vis + 32;              // [2] value exponent; [2][4] warps' maxima
   static constexpr int bars = ve + 48;             // 10 mbarriers
@@ -118,6 +125,14 @@ __device__ __forceinline__ void ld_16x128(uint32_t t, uint32_t (&r)[8]) {
                : "r"(t));
 }
 
+// Waits for this warp's tensor memory loads; x is not to be read before.
+__device__ __forceinline__ void ld_wait(uint32_t (&x)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]), "+r"(x[8]),
+                 "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
+               :: "memory");
+}
+
 // Place of feature f in a code tile's row (in elements) when its codes have nc = 32 / b a word: quarter
 // row m, piece i of it (pairs 4i .. 4i+3 of code_pair's order), at piece i * 4 + m.
 __device__ __forceinline__ int place_of(int f, int nc, int D) {
@@ -126,64 +141,71 @@ __device__ __forceinline__ int place_of(int f, int nc, int D) {
   return ((pair >> 2) * 4 + m) * 8 + (pair & 3) * 2 + c / (nc / 2);
 }
 
-// Swaps the raw codes of pieces 0 and 1, 2 and 3 of a lane's quarter row (odd token rows: then the eight
-// lanes of a store phase, two rows of four quarters, meet all eight 16-byte slots).
-template <int D, int B>
-__device__ __forceinline__ void swap_pieces(uint32_t (&w)[D * B / 128], bool odd) {
-  constexpr int W = D * B / 128;
-  if constexpr (B == 2) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __byte_perm(w[i], 0, odd ? 0x2301 : 0x3210);
-  } else {
-    constexpr int P = B / 4;  // words a piece
-#pragma unroll
-    for (int i = 0; i < W; i += 2 * P)
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const uint32_t x = w[i + j], y = w[i + P + j];
-        w[i + j] = odd ? y : x;
-        w[i + P + j] = odd ? x : y;
-      }
-  }
+// The widening warps hold a token row in four lanes, lane = 8 m + g: row it*8 + g, quarter m. The eight lanes of
+// a 16-byte store phase then have one piece of eight rows, which the swizzle puts into eight slots.
+//
+// Keys: codes are whole numbers c 2^-24 already as the f16 bits of their fields (f16's subnormals, with a
+// field's place in its byte a further power of two that R q is divided by): one mask a pair.
+template <int B, int W>
+__device__ __forceinline__ uint32_t field_pair(const uint32_t (&w)[W], int i) {
+  constexpr int H = 16 / B, F = 8 / B;  // pairs a word, fields a byte
+  const int p = i % H;
+  const uint32_t x = p >= F ? w[i / H] >> 8 : w[i / H];
+  return x & (0x00010001u * (((1u << B) - 1) << (B * (p % F))));
 }
-
-// This warp's 32 token rows of raw codes (row it*8 + g, quarter m) to f16 pieces in the tile. off[i]: where
-// piece i (after the swap) goes in the row group's 8 rows; row groups are 1024 bytes apart.
 template <int D, int B>
-__device__ __forceinline__ void widen(uint32_t (&w)[4][D * B / 128], uint8_t* tile, const int (&off)[D / 32], bool odd) {
+__device__ __forceinline__ void widen_keys(const uint32_t (&w)[4][D * B / 128], uint8_t* tile, const int (&off)[D / 32]) {
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    swap_pieces<D, B>(w[it], odd);
+  for (int it = 0; it < 4; ++it)
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t h[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) h[x] = code_pair<B, D * B / 128>(w[it], 4 * i + x);
+      for (int x = 0; x < 4; ++x) h[x] = field_pair<B, D * B / 128>(w[it], 4 * i + x);
+      *reinterpret_cast<uint4*>(tile + off[i] + it * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+// Values: dequantised, code * scale + zero in f16 by one fused multiply-add from the field's bits, in units of
+// 2^(ve - kVExp): scale[F] holds scale * 2^(24 - place) for the F places of a field in its byte.
+template <int D, int B>
+__device__ __forceinline__ void widen_values(const uint32_t (&w)[4][D * B / 128], const float2 (&sz)[4], uint8_t* tile,
+                                             const int (&off)[D / 32]) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    constexpr int F = 8 / B;
+    uint32_t s[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) s[f] = h2_pack(sz[it].x * pow2i(-B * f), sz[it].x * pow2i(-B * f));
+    const uint32_t z = h2_pack(sz[it].y, sz[it].y);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t h[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) h[x] = h2_fma(field_pair<B, D * B / 128>(w[it], 4 * i + x), s[(4 * i + x) % F], z);
       *reinterpret_cast<uint4*>(tile + off[i] + it * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
 }
+// Where the lane's pieces of its row group go; row groups are 1024 bytes apart.
 template <int D>
 __device__ __forceinline__ void piece_offsets(int row0, int g, int m, int (&off)[D / 32]) {
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const int piece = (i ^ (g & 1)) * 4 + m;
+    const int piece = i * 4 + m;
     off[i] = (piece >> 3) * (128 * 128) + (row0 + g) * 128 + (((piece & 7) ^ g) << 4);
   }
 }
 
-// Raw codes of this warp's 32 token rows: rows of page pg[it] (-1: zeros).
+// Raw codes of this warp's 32 token rows in segment seg of their pages (nullptr: zeros).
 template <int D, int B>
-__device__ __forceinline__ void load_raw(const PagesDev& p, uint32_t seg, const int (&pg)[4], int h, int tok0, int g, int m,
-                                         uint32_t (&w)[4][D * B / 128]) {
+__device__ __forceinline__ void load_raw(const PagesDev& p, uint32_t seg, const uint8_t* const (&page)[2], int h, int tok0, int g,
+                                         int m, uint32_t (&w)[4][D * B / 128]) {
   constexpr int W = D * B / 128;
   const int ps = 1 << p.ps_log2;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
-    if (pg[it] >= 0) {
-      const uint8_t* src = p.pool + uint64_t(pg[it]) * p.page_bytes + seg +
-                           (uint32_t(h) * ps + ((tok0 + it * 8 + g) & (ps - 1))) * uint32_t(D * B / 8) + m * (4 * W);
-      load_words<W>(src, w[it]);
+    if (page[it >> 1]) {
+      load_words<W>(page[it >> 1] + seg + (uint32_t(h) * ps + ((tok0 + it * 8 + g) & (ps - 1))) * uint32_t(D * B / 8) + m * (4 * W), w[it]);
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i) w[it][i] = 0;
@@ -196,6 +218,7 @@ struct Ctx {
   uint8_t* smem;
   uint32_t sb, bar0;
   int n_tiles, tile0, len, h, b;
+  float unscale;  // of the scores' accumulators
   __device__ __forceinline__ uint32_t k_full(int s) const { return bar0 + 8 * s; }
   __device__ __forceinline__ uint32_t v_full(int s) const { return bar0 + 16 + 8 * s; }
   __device__ __forceinline__ uint32_t s_done(int s) const { return bar0 + 32 + 8 * s; }
@@ -207,42 +230,57 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, int parity, int32_t* err)
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 
-// Pages of the four 8-token row groups that a warp widens (-1: past the end, or no page).
+// Table entries of the two 16-token halves of a warp's 32 tokens, read a tile before they are needed, and
+// the pages they name (-1: past the end, or no page, which is reported).
 template <int D>
-__device__ __forceinline__ void tile_pages(const TreeArgs& a, const Ctx<D>& c, int tok0, int (&pg)[4]) {
+struct Halves {
+  int id[2];
+  __device__ __forceinline__ void read(const TreeArgs& a, const Ctx<D>& c, int tok0) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half)
-    pg[2 * half] = pg[2 * half + 1] = tok0 + half * 16 < c.len ? page_of(a.p, c.b, tok0 + half * 16, a.err) : -1;
-}
+    for (int x = 0; x < 2; ++x) {
+      id[x] = -1;
+      if (tok0 + 16 * x < c.len) id[x] = a.p.table[int64_t(c.b) * a.p.max_pages + ((tok0 + 16 * x) >> a.p.ps_log2)];
+    }
+  }
+  __device__ __forceinline__ const uint8_t* page(const TreeArgs& a, const Ctx<D>& c, int tok0, int x) const {
+    if (uint32_t(id[x]) >= uint32_t(a.p.n_pages)) {
+      if (tok0 + 16 * x < c.len) report_error(a.err, JOLT_ERR_INVALID_ARG);
+      return nullptr;
+    }
+    return a.p.pool + uint64_t(uint32_t(id[x])) * a.p.page_bytes;
+  }
+};
 
-// Warps 8-11: the keys' codes to f16 tiles, and per token pair (scale, zero) of keys and values as the
-// softmax uses them. After a wait that gave up (reported) a warp only keeps step at the named barrier.
+// Warps 16-19: the keys' codes to f16 tiles, the keys' (scale, zero) per token pair as the softmax uses them,
+// and the exponent of the values' largest magnitude so far (ve): the values are widened in units of 2^(ve - kVExp).
+// After a wait that gave up (reported) a warp only keeps step at the named barrier.
 template <int D, int BK>
 __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) {
   using S = Smem<D>;
-  const int g = lane >> 2, m = lane & 3;
+  const int g = lane & 7, m = lane >> 3;
   const int ps = 1 << a.p.ps_log2;
   uint32_t w[4][D * BK / 128];
   int off[D / 32];
   piece_offsets<D>(wq * 32, g, m, off);
-  const float ko = float(1 << (BK - 1)), vo = float(1 << (a.p.bv - 1));
+  const float vtop = float((1 << a.p.bv) - 1);
   __half2 ksz, vsz;
   bool seen;
+  Halves<D> hv;
   auto fetch = [&](int n) {
-    int pg[4];
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    tile_pages<D>(a, c, tok0, pg);
-    load_raw<D, BK>(a.p, a.p.kc, pg, c.h, tok0, g, m, w);
-    const int page = lane < 16 ? pg[0] : pg[2];  // the lane's own token
-    seen = page >= 0 && tok0 + lane < c.len;
+    const uint8_t* const page[2] = {hv.page(a, c, tok0, 0), hv.page(a, c, tok0, 1)};
+    hv.read(a, c, tok0 + kTok);
+    load_raw<D, BK>(a.p, a.p.kc, page, c.h, tok0, g, m, w);
+    const uint8_t* base = lane < 16 ? page[0] : page[1];  // the lane's own token
+    seen = base && tok0 + lane < c.len;
     ksz = vsz = __floats2half2_rn(0.f, 0.f);
     if (seen) {
-      const uint8_t* base = a.p.pool + uint64_t(page) * a.p.page_bytes;
       const uint32_t row = uint32_t(c.h) * ps + ((tok0 + lane) & (ps - 1));
       ksz = reinterpret_cast<const __half2*>(base + a.p.ks)[row];
       vsz = reinterpret_cast<const __half2*>(base + a.p.vs)[row];
     }
   };
+  hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
   int ve = -30;
   float* red = reinterpret_cast<float*>(c.smem + S::ve + 8);
@@ -250,10 +288,11 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   for (int n = 0; n < c.n_tiles; ++n) {
     const int s = n & 1, prev = ((n >> 1) & 1) ^ 1;  // parity of the phase that tile n - 2 completed
     if (n >= 2) ok = ok && wait_all(c.s_done(s), prev, a.err);
-    if (ok) widen<D, BK>(w, c.smem + S::k + s * S::kTile, off, g & 1);
+    if (ok) widen_keys<D, BK>(w, c.smem + S::k + s * S::kTile, off);
     const float2 kf = __half22float2(ksz), vf = __half22float2(vsz);
     const uint32_t word = __ballot_sync(0xffffffffu, seen);
-    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vf.x)));
+    const float most = fmaxf(fabsf(vf.y), fabsf(vf.y + vtop * vf.x));
+    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     if (n + 1 < c.n_tiles) fetch(n + 1);
     // the softmax of tile n - 2 is done with this buffer's scales
     if (n >= 2) ok = ok && wait_all(c.p_full(s), prev, a.err);
@@ -266,13 +305,11 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = fmaxf(top, red[s * 4 + i]);
-    ve = max(ve, int(__float_as_uint(top) >> 23) - 126);
+    ve = min(max(ve, int(__float_as_uint(top) >> 23) - 126), 30);
     const bool here = (word >> lane) & 1;
-    float* dst = reinterpret_cast<float*>(c.smem + S::sc + s * 2048) + (wq * 16 + (lane >> 1)) * 8 + (lane & 1);
-    dst[0] = here ? kf.x : 0.f;
-    dst[2] = here ? kf.y + ko * kf.x : 0.f;
-    dst[4] = here ? vf.x * pow2i(kPExp - ve) : 0.f;
-    dst[6] = here ? vf.y + vo * vf.x : 0.f;
+    float* dst = reinterpret_cast<float*>(c.smem + S::sc + s * 1024) + (wq * 16 + (lane >> 1)) * 4 + (lane & 1);
+    dst[0] = here ? kf.x * c.unscale : 0.f;
+    dst[2] = here ? kf.y : 0.f;
     if (wq == 0 && lane == 0) reinterpret_cast<int*>(c.smem + S::ve)[s] = ve;
     fence_proxy_async_smem();
     __syncwarp();
@@ -280,25 +317,44 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   }
 }
 
-// Warps 12-15: the values' codes to f16 tiles.
+// Warps 20-23: the values to f16 tiles. A token that is not seen gets zeros (its scale may be anything).
 template <int D, int BV>
 __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) {
   using S = Smem<D>;
-  const int g = lane >> 2, m = lane & 3;
+  const int g = lane & 7, m = lane >> 3;
+  const int ps = 1 << a.p.ps_log2;
   uint32_t w[4][D * BV / 128];
+  __half2 raw[4];
   int off[D / 32];
   piece_offsets<D>(wq * 32, g, m, off);
+  Halves<D> hv;
   auto fetch = [&](int n) {
-    int pg[4];
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    tile_pages<D>(a, c, tok0, pg);
-    load_raw<D, BV>(a.p, a.p.vc, pg, c.h, tok0, g, m, w);
+    const uint8_t* const page[2] = {hv.page(a, c, tok0, 0), hv.page(a, c, tok0, 1)};
+    hv.read(a, c, tok0 + kTok);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int tok = tok0 + it * 8 + g;
+      raw[it] = __floats2half2_rn(0.f, 0.f);
+      if (page[it >> 1] && tok < c.len)
+        raw[it] = reinterpret_cast<const __half2*>(page[it >> 1] + a.p.vs)[uint32_t(c.h) * ps + (tok & (ps - 1))];
+    }
+    load_raw<D, BV>(a.p, a.p.vc, page, c.h, tok0, g, m, w);
   };
+  hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
   for (int n = 0; n < c.n_tiles; ++n) {
-    const int s = n & 1, prev = ((n >> 1) & 1) ^ 1;
-    if (n >= 2 && !wait_all(c.pv_done(s), prev, a.err)) return;
-    widen<D, BV>(w, c.smem + S::v + s * S::kTile, off, g & 1);
+    const int s = n & 1, par = (n >> 1) & 1;
+    if (!wait_all(c.k_full(s), par, a.err)) return;  // ve of this tile
+    const float down = pow2i(kVExp<BV> - reinterpret_cast<const int*>(c.smem + S::ve)[s]);
+    float2 sz[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const float2 f = __half22float2(raw[it]);
+      sz[it] = make_float2(f.x * down * 16777216.f, f.y * down);
+    }
+    if (n >= 2 && !wait_all(c.pv_done(s), par ^ 1, a.err)) return;
+    widen_values<D, BV>(w, sz, c.smem + S::v + s * S::kTile, off);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.v_full(s));
@@ -306,7 +362,7 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   }
 }
 
-// Warp 16: scores of tile n, then outputs of tile n - 1.
+// Warp 24: scores of tile n, then outputs of tile n - 1.
 template <int D>
 __device__ void mma_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int lane) {
   using S = Smem<D>;
@@ -352,48 +408,45 @@ __device__ void mma_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int 
   }
 }
 
-// Softmax of one stream. Thread (g, m) of warp wq has rows 32 wq + {g, g+8, g+16, g+24} and the tokens
-// 8j + 2m, 8j + 2m + 1: four lanes share a row, and a token pair's scales serve four rows.
-// With t = scale_k acc + zero_k qs (scores are rs t): p = 2^(rs t - ref). ref is a whole number, at least
-// the row's maximum when it was last set. It is set anew only when a score passes it by 2^8 (p * scale
-// then still fits f16), which after a row's first tokens is rare; what was formed under the old one (this
-// tile's P, the sums, O) is multiplied by a power of two.
+// Softmax of 16 rows of one stream. Thread (g, m) has rows row0 + g and row0 + g + 8 and the tokens 8j + 2m,
+// 8j + 2m + 1: four lanes share a row, and a token pair's scales serve two rows.
+// With s = scale_k acc + zero_k qs: p = 2^(s - ref + 7). ref is a whole number, 4 above
+// the row's maximum when it was last set. It is set anew only when a thread's eight p of a chunk add up to
+// more than 2^15 (some score then passed it by 5 or more; until then p fits f16), which after a row's first
+// tokens is rare: the usual pass needs no maximum. What was formed under the old reference (this tile's P,
+// the sum, O) is then multiplied by a power of two. That took 8% of the chunks, and a third of the
+// kernel's time, when ref was set to the maximum itself.
 template <int D>
-__device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int strm, int wq, int lane, int r0,
+__device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int strm, int row0, int lane, int r0,
                              int rows, int split) {
   using S = Smem<D>;
   const int g = lane >> 2, m = lane & 3;
-  const uint32_t ts = tmem + strm * 128 + (uint32_t(wq * 32) << 16);
-  const uint32_t to = tmem + 256 + strm * 128 + (uint32_t(wq * 32) << 16);
-  constexpr uint32_t kLow = 16u << 16;  // the quarter's lanes 16-31
-  float rs[4], ref[4], qs[4];
-  f2 l2[4], z2[4];
+  const uint32_t ts = tmem + strm * 128 + (uint32_t(row0) << 16);
+  const uint32_t to = tmem + 256 + strm * 128 + (uint32_t(row0) << 16);
+  float ref[2];
+  f2 l2[2], qs2[2], neg2[2];  // neg2: 7 - ref; +inf before the first: every p is then too large
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    rs[r] = reinterpret_cast<const float*>(c.smem + S::rs)[wq * 32 + g + 8 * r];
-    qs[r] = reinterpret_cast<const float*>(c.smem + S::qs)[wq * 32 + g + 8 * r];
+  for (int r = 0; r < 2; ++r) {
+    const float qs = reinterpret_cast<const float*>(c.smem + S::qs)[row0 + g + 8 * r];
+    qs2[r] = f2_make(qs, qs);
+    neg2[r] = f2_make(INFINITY, INFINITY);
     ref[r] = -INFINITY;
-    l2[r] = z2[r] = f2_make(0.f, 0.f);
+    l2[r] = f2_make(0.f, 0.f);
   }
   int ve = -30;
   bool ok = true;
-  // O of this stream times f, after the last product into it (tile n - 2's)
-  auto scale_o = [&](const float (&f)[4], int par) {
+  // O of these rows times f, after the last product into it (tile n - 2's)
+  auto scale_o = [&](float f0, float f1, int par) {
     if (!wait_all(c.pv_done(strm), par ^ 1, a.err)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int ch = 0; ch < D / 32; ++ch) {
-      uint32_t x[2][16];
-      ld_16x256(to + ch * 32, x[0]);
-      ld_16x256(to + kLow + ch * 32, x[1]);
-      tmem_ld_wait();
+      uint32_t x[16];
+      ld_16x256(to + ch * 32, x);
+      ld_wait(x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[0][i] = __float_as_uint(__uint_as_float(x[0][i]) * f[(i >> 1) & 1]);
-        x[1][i] = __float_as_uint(__uint_as_float(x[1][i]) * f[2 + ((i >> 1) & 1)]);
-      }
-      st_16x256(to + ch * 32, x[0]);
-      st_16x256(to + kLow + ch * 32, x[1]);
+      for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * ((i & 2) ? f1 : f0));
+      st_16x256(to + ch * 32, x);
     }
     tmem_st_wait();
     return true;
@@ -403,104 +456,108 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
     ok = wait_all(c.k_full(strm), par, a.err) && wait_all(c.s_done(strm), par, a.err);
     if (!ok) break;
     tc_fence_after();
-    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(c.smem + S::sc + strm * 2048);
+    uint32_t x[16];
+    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(c.smem + S::sc + strm * 1024) + m;
     const uint32_t* vis = reinterpret_cast<const uint32_t*>(c.smem + S::vis) + strm * 4;
     const int ve_now = reinterpret_cast<const int*>(c.smem + S::ve)[strm];
     if (ve_now != ve) {
       const float drop = pow2i(max(ve - ve_now, -126));
-      const float f[4] = {drop, drop, drop, drop};
       ve = ve_now;
-      if (n >= 2) ok = scale_o(f, par);
-      if (!ok) break;
+      if (n >= 2) {
+        ok = scale_o(drop, drop, par);
+        if (!ok) break;
+      }
     }
     const bool whole = (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu;
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      uint32_t x[2][16];
-      ld_16x256(ts + ch * 32, x[0]);
-      ld_16x256(ts + kLow + ch * 32, x[1]);
-      tmem_ld_wait();
-      f2 t[4][4];
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    bool tried = false;
+#pragma unroll 1  // one copy of the body: the roles' code together is already long for the instruction cache
+    for (int ch = 0; ch < 4;) {
+      ld_16x256(ts + ch * 32, x);
+      ld_wait(x);
+      f2 e2[4][2];
 #pragma unroll
       for (int at = 0; at < 4; ++at) {
-        const ulonglong2 k = sc[((ch * 4 + at) * 4 + m) * 2];
+        const ulonglong2 k = sc[(ch * 4 + at) * 4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f2 acc = f2_make(__uint_as_float(x[r >> 1][4 * at + 2 * (r & 1)]), __uint_as_float(x[r >> 1][4 * at + 2 * (r & 1) + 1]));
-          t[at][r] = f2_fma(acc, k.x, f2_mul(k.y, f2_make(qs[r], qs[r])));
-        }
+        for (int r = 0; r < 2; ++r)
+          e2[at][r] = f2_fma(f2_make(__uint_as_float(x[4 * at + 2 * r]), __uint_as_float(x[4 * at + 2 * r + 1])), k.x,
+                             f2_fma(k.y, qs2[r], neg2[r]));
       }
       if (!whole) {
         const uint32_t word = vis[ch] >> (2 * m);
 #pragma unroll
         for (int at = 0; at < 4; ++at)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float2 f = f2_get(t[at][r]);
+          for (int r = 0; r < 2; ++r) {
+            float2 f = f2_get(e2[at][r]);
             if (!((word >> (8 * at)) & 1)) f.x = -INFINITY;
             if (!((word >> (8 * at)) & 2)) f.y = -INFINITY;
-            t[at][r] = f2_make(f.x, f.y);
+            e2[at][r] = f2_make(f.x, f.y);
           }
       }
-      bool past = false;
+      uint32_t pk[8];
+      f2 sum[2];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int at = 0; at < 4; ++at) {
-          const float2 f = f2_get(t[at][r]);
-          top[r] = fmaxf(top[r], fmaxf(f.x, f.y));
+          const float2 e = f2_get(e2[at][r]);
+          const float p0 = ex2(e.x), p1 = ex2(e.y);
+          sum[r] = at ? f2_add(sum[r], f2_make(p0, p1)) : f2_make(p0, p1);
+          pk[2 * at + r] = h2_pack(p0, p1);
         }
-        past = past || top[r] * rs[r] > ref[r] + kSlack;
-      }
-      if (__any_sync(0xffffffffu, past)) {
-        float f[4];
+      const float2 s0 = f2_get(sum[0]), s1 = f2_get(sum[1]);
+      if (!tried && __any_sync(0xffffffffu, fmaxf(s0.x + s0.y, s1.x + s1.y) > kMost)) {
+        // new references, from this chunk's scores read again; then the chunk once more
+        tried = true;
+        float top[2] = {-INFINITY, -INFINITY}, f[2];
+        ld_16x256(ts + ch * 32, x);
+        ld_wait(x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x1 = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)) * rs[r];
-          const float now = x1 > ref[r] + kSlack ? ceilf(x1) : ref[r];
+        for (int at = 0; at < 4; ++at) {
+          const ulonglong2 k = sc[(ch * 4 + at) * 4];
+          const uint32_t word = vis[ch] >> (2 * m + 8 * at);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 t = f2_get(f2_fma(f2_make(__uint_as_float(x[4 * at + 2 * r]), __uint_as_float(x[4 * at + 2 * r + 1])),
+                                           k.x, f2_mul(k.y, qs2[r])));
+            if (word & 1) top[r] = fmaxf(top[r], t.x);
+            if (word & 2) top[r] = fmaxf(top[r], t.y);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+          const float now = fmaxf(ref[r], ceilf(top[r]) + kRoom);
           f[r] = now == ref[r] ? 1.f : ex2(ref[r] - now);
           ref[r] = now;
           l2[r] = f2_mul(l2[r], f2_make(f[r], f[r]));
-          z2[r] = f2_mul(z2[r], f2_make(f[r], f[r]));
+          const float neg = kPExp - now;
+          neg2[r] = f2_make(neg, neg);
         }
         tmem_st_wait();
 #pragma unroll 1
-        for (int e = 0; e < ch; ++e)
+        for (int e = 0; e < ch; ++e) {
+          uint32_t y[8];
+          ld_16x128(ts + e * 32, y);
+          tmem_ld_wait();
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t y[8];
-            ld_16x128(ts + hh * kLow + e * 32, y);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn(f[2 * hh + (i & 1)]));
-              y[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            st_16x128(ts + hh * kLow + e * 32, y);
+          for (int i = 0; i < 8; ++i) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn(f[i & 1]));
+            y[i] = *reinterpret_cast<const uint32_t*>(&v);
           }
-        if (n >= 2) ok = scale_o(f, par);
-        if (!ok) break;
-      }
-      uint32_t pk[2][8];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float neg = ref[r] == -INFINITY ? 0.f : -ref[r];
-        const f2 neg2 = f2_make(neg, neg), rs2 = f2_make(rs[r], rs[r]);
-#pragma unroll
-        for (int at = 0; at < 4; ++at) {
-          const ulonglong2 v = sc[((ch * 4 + at) * 4 + m) * 2 + 1];
-          const float2 e = f2_get(f2_fma(t[at][r], rs2, neg2));
-          const f2 p = f2_make(ex2(e.x), ex2(e.y));
-          l2[r] = f2_add(l2[r], p);
-          z2[r] = f2_fma(p, v.y, z2[r]);
-          const float2 w = f2_get(f2_mul(p, v.x));
-          pk[r >> 1][2 * at + (r & 1)] = h2_pack(w.x, w.y);
+          st_16x128(ts + e * 32, y);
         }
+        if (n >= 2) ok = scale_o(f[0], f[1], par);
+        if (!ok) break;
+        continue;
       }
-      st_16x128(ts + ch * 32, pk[0]);
-      st_16x128(ts + kLow + ch * 32, pk[1]);
+      tried = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) l2[r] = f2_add(l2[r], sum[r]);
+      st_16x128(ts + ch * 32, pk);
+      ++ch;
     }
     if (!ok) break;
     tmem_st_wait();
@@ -514,26 +571,21 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
     ok = wait_all(c.pv_done(strm), (mine - 1) & 1, a.err);
     tc_fence_after();
   }
-  const float unit = pow2i(ve - kPExp);
-  float z[4];
-  float* dst[4];
+  const float unit = pow2i(ve - (a.p.bv - 10));  // kVExp
+  float* dst[2];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float2 lf = f2_get(l2[r]), zf = f2_get(z2[r]);
+  for (int r = 0; r < 2; ++r) {
+    const float2 lf = f2_get(l2[r]);
     float l = lf.x + lf.y;
-    z[r] = zf.x + zf.y;
 #pragma unroll
-    for (int x = 1; x <= 2; x <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, x);
-      z[r] += __shfl_xor_sync(0xffffffffu, z[r], x);
-    }
-    const int row = wq * 32 + g + 8 * r;
+    for (int x = 1; x <= 2; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const int row = row0 + g + 8 * r;
     dst[r] = nullptr;
     if (row < rows) {
       const int q = r0 + row;
       const int64_t gr = (int64_t(c.b) * a.n_new + q / a.gq) * a.n_q + c.h * a.gq + q % a.gq;
       const int64_t part = gr * a.parts + 2 * split + strm;
-      if (m == 0) a.ml[part] = make_float2(ref[r], l);
+      if (m == 0) a.ml[part] = make_float2(ref[r] - kPExp, l);  // p and O were carried times 2^7
       if (ref[r] != -INFINITY) dst[r] = a.acc + part * D;
     }
   }
@@ -541,19 +593,18 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
   const int nc = 32 / a.p.bv, hn = nc / 2;
 #pragma unroll 1
   for (int ch = 0; ch < D / 32; ++ch) {
-    uint32_t x[2][16];
-    ld_16x256(to + ch * 32, x[0]);
-    ld_16x256(to + (16u << 16) + ch * 32, x[1]);
-    tmem_ld_wait();
+    uint32_t x[16];
+    ld_16x256(to + ch * 32, x);
+    ld_wait(x);
+    const int pair = ch * 4 + m;  // piece ch * 4 + at: quarter row `at`, pairs 4 ch ..
 #pragma unroll
     for (int at = 0; at < 4; ++at) {
-      const int pair = ch * 4 + m;  // piece ch * 4 + at: quarter row `at`, pairs 4 ch ..
       const int f = at * (D / 4) + (pair / hn) * nc + pair % hn;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 2; ++r)
         if (dst[r]) {
-          dst[r][f] = __uint_as_float(x[r >> 1][4 * at + 2 * (r & 1)]) * unit + z[r];
-          dst[r][f + hn] = __uint_as_float(x[r >> 1][4 * at + 2 * (r & 1) + 1]) * unit + z[r];
+          dst[r][f] = __uint_as_float(x[4 * at + 2 * r]) * unit;
+          dst[r][f + hn] = __uint_as_float(x[4 * at + 2 * r + 1]) * unit;
         }
     }
   }
@@ -570,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   const int split = int(blockIdx.x) - draft_x;  // the drafted tokens' blocks come first: they are short
   uint8_t* smem = align_smem_1024(raw);
   if (split < 0) {
-    draft_block<__nv_bfloat16, D, kRows, kThreads>(a, b, h, r0, smem);
+    draft_part<__nv_bfloat16, D, kRows, kThreads>(a, b, h, r0, smem);
     return;
   }
   const int rows = min(kRows, draft_count(a, b) * a.gq - r0);
@@ -586,65 +637,79 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   c.tile0 = split * per;
   c.n_tiles = max(0, min(tiles, c.tile0 + per) - c.tile0);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::slot);
-  if (warp == 16) {
+  if (warp == 24) {
     tmem_alloc(smem_u32(slot), 512);
     if (lane == 0) {
       for (int s = 0; s < 2; ++s) {
         mbar_init(c.k_full(s), 4);
         mbar_init(c.v_full(s), 4);
         mbar_init(c.s_done(s), 1);
-        mbar_init(c.p_full(s), 4);
+        mbar_init(c.p_full(s), 8);
         mbar_init(c.pv_done(s), 1);
       }
       fence_mbar_init();
     }
     __syncwarp();
   }
-  // R q as two f16 terms, scaled by a power of two of the row
+  // R q as two f16 terms, scaled by one power of two for all rows: the largest element then has 2^14, and the
+  // second term's last place is 2^-24, 2^-39 of it
   {
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
     const float isd = rsqrtf(float(D));
     const int nc = 32 / a.p.bk;
     int at[E];
+    float sign[E], low[E];  // low: 2^-(a code field's place in its byte)
 #pragma unroll
-    for (int e = 0; e < E; ++e) at[e] = place_of(lane * E + e, nc, D);
-    float sign[E];
+    for (int e = 0; e < E; ++e) {
+      at[e] = place_of(lane * E + e, nc, D);
+      sign[e] = rot_sign(a.p.seed, lane * E + e);
+      low[e] = pow2i(-a.p.bk * (((at[e] & 7) >> 1) % (8 / a.p.bk)));
+    }
+    constexpr int kW = kThreads / 32, kPer = (kRows + kW - 1) / kW;
+    float v[kPer][E], top = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sign[e] = rot_sign(a.p.seed, lane * E + e);
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-      float v[E];
+    for (int i = 0; i < kPer; ++i) {
+      const int r = warp + i * kW;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
       if (r < rows) {
         const int row = r0 + r;
         const __nv_bfloat16* x = qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = ld_as_float(x, e) * a.scale2 * sign[e];
+        for (int e = 0; e < E; ++e) v[i][e] = ld_as_float(x, e) * a.scale2 * sign[e];
       }
-      warp_fwht<E>(v);
-      float top = 0.f, sum = 0.f;
+      warp_fwht<E>(v[i]);
+      float sum = 0.f, most = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        v[e] *= isd;
-        top = fmaxf(top, fabsf(v[e]));
-        sum += v[e];
+        v[i][e] *= isd;
+        most = fmaxf(most, fabsf(v[i][e]));
+        sum += v[i][e];
       }
-      top = warp_max(top);
+      if (most < INFINITY) top = fmaxf(top, most);  // a row that is not finite is on its own
       sum = warp_sum(sum);
-      int k = 0;
-      if (top > 0.f && top < INFINITY) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
-      const float up = pow2i(k);
+      if (lane == 0 && r < kRows) reinterpret_cast<float*>(smem + S::qs)[r] = sum;
+    }
+    top = warp_max(top);
+    if (lane == 0) reinterpret_cast<float*>(smem + S::rs)[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kW; ++i) top = fmaxf(top, reinterpret_cast<const float*>(smem + S::rs)[i]);
+    int k = 0;
+    if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
+    c.unscale = pow2i(24 - k);
+    const float up = pow2i(k);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = warp + i * kW;
+      if (r >= kRows) break;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float x = v[e] * up;
+        const float x = v[i][e] * up * low[e];
         const __half x1 = __float2half_rn(x), x2 = __float2half_rn(x - __half2float(x1));
         const int off = (at[e] >> 6) * S::kChunk + r * 128 + ((((at[e] >> 3) & 7) ^ (r & 7)) << 4) + (at[e] & 7) * 2;
         *reinterpret_cast<__half*>(smem + S::q + off) = x1;
         *reinterpret_cast<__half*>(smem + S::q + S::kTile + off) = x2;
-      }
-      if (lane == 0) {
-        reinterpret_cast<float*>(smem + S::rs)[r] = pow2i(-k);
-        reinterpret_cast<float*>(smem + S::qs)[r] = sum * up;
       }
     }
   }
@@ -653,14 +718,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  if (warp < 8) {
+  if (warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoft));
-    softmax_role<D>(a, c, tmem, warp >> 2, warp & 3, lane, r0, rows, split);
-  } else if (warp < 16) {
+    // a warp reaches the 32 lanes of its quarter, warp % 4
+    softmax_role<D>(a, c, tmem, warp >> 3, (warp & 3) * 32 + ((warp >> 2) & 1) * 16, lane, r0, rows, split);
+  } else if (warp < 24) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWiden));
     if (c.n_tiles > 0) {
-      const int bits = warp < 12 ? a.p.bk : a.p.bv;
-      if (warp < 12) {
+      const int bits = warp < 20 ? a.p.bk : a.p.bv;
+      if (warp < 20) {
         if (bits == 4) keys_role<D, 4>(a, c, warp & 3, lane);
         else if (bits == 8) keys_role<D, 8>(a, c, warp & 3, lane);
         else keys_role<D, 2>(a, c, warp & 3, lane);
@@ -672,11 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
-    if (warp == 16) mma_role<D>(a, c, tmem, lane);
+    if (warp == 24) mma_role<D>(a, c, tmem, lane);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 24) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -702,7 +768,7 @@ jolt_status launch(const TreeArgs& a, bool draft, size_t smem, cudaStream_t st) 
 }  // namespace
 
 size_t tree_tc_smem(int d_h) {
-  const size_t draft = size_t(kMaxDraft) * (2 * d_h + 4) * 4 + size_t(kRows) * d_h * 4 + kThreads / 32 * 4 * 64 * 4 + 1024;
+  const size_t draft = draft_smem(d_h, kRows, kThreads) + 1024;
   return std::max<size_t>(d_h == 128 ? Smem<128>::total : Smem<64>::total, draft);
 }
 

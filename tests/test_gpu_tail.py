@@ -352,6 +352,22 @@ def test_attention_ignores_what_masked_places_hold(cuda_ok, io):
             assert torch.equal(a[0, keep], w[0, keep]) and torch.equal(a[1], w[1])
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n,nq", [(4, 4), (40, 2)])
+def test_attention_rows_that_see_infinite_values(cuda_ok, io, n, nq):
+    c = attn_case(51, [30], n, nq, 1, 64, 4, 4, 16, io)
+    v, mask = c[6], c[7]
+    want = run_attn(c)
+    v[0, 2, 0, 7], v[0, 3, 0, 9] = float("inf"), float("nan")
+    out, lse = run_attn(c)
+    sees = [(mask[0] >> j) & 1 == 1 for j in (2, 3)]
+    assert bool((out[0, sees[0] & ~sees[1], :, 7] == math.inf).all()) and bool(out[0, sees[1], :, 9].isnan().all())
+    free = ~sees[0] & ~sees[1]
+    assert torch.equal(out[0, free], want[0][0, free]) and torch.equal(lse, want[1])
+    keep = [f for f in range(64) if f not in (7, 9)]
+    assert torch.equal(out[0][..., keep], want[0][0][..., keep])
+
+
 def test_attention_strides_no_lse_and_prefix_in_place(cuda_ok):
     rng = np.random.default_rng(46)
     c = attn_case(45, [65, 130], 3, 8, 2, 128, 4, 8, 64, "bf16", prefix=True)
