@@ -247,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   const float ok_off = float(1 << (a.p.bk - 1)), ov_off = float(1 << (a.p.bv - 1));
   for (int n = 0; n < n_mine; ++n) {
     const int st = n % a.stages;
-    if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (n / a.stages) & 1, a.err))) {
+    if (!wait_all(bar0 + 8 * st, (n / a.stages) & 1, a.err)) {
       // gave up (reported): wait, with the same limit, for what is still in flight, then stop
       for (int x = n + 1; x < min(n + a.stages, n_mine); ++x)
-        mbar_wait(bar0 + 8 * (x % a.stages), (x / a.stages) & 1, a.err);
+        wait_all(bar0 + 8 * (x % a.stages), (x / a.stages) & 1, a.err);
       break;
     }
     const uint8_t* kc = ring + st * a.stage_bytes;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   const float* acc = a.acc + row * a.parts * D + lane * E;
-  for (int s = 0; s < a.cached; ++s) {
+  for (int s = 0; s < a.splits; ++s) {
     const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
     if (f != 0.f) {
 #pragma unroll
@@ -487,10 +487,10 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] *= back[e];
   if (draft) {
-    const float f = __shfl_sync(0xffffffffu, a.cached < 32 ? w[0] : w[1], a.cached & 31);
+    const float f = __shfl_sync(0xffffffffu, a.splits < 32 ? w[0] : w[1], a.splits & 31);
     if (f != 0.f) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.cached) * D + e];
+      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.splits) * D + e];
     }
   }
   if (wp != 0.f) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 // ---- host -------------------------------------------------------------------------------------------
 
 struct TreePlan {
-  int nt, blocks, splits, cached, parts, stages, stage_bytes;
+  int nt, blocks, splits, parts, stages, stage_bytes;
   bool pack, tc;
   size_t smem, ws_acc, ws_total;
 };
@@ -521,8 +521,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
     t.blocks = (rows + 127) / 128;
     const int64_t units = int64_t(batch) * p.n_kv * t.blocks;
     const int64_t tiles = (int64_t(max_pages) * p.page_size + 127) / 128;
-    t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits / 2, (tiles + 1) / 2, 148 / units})));
-    t.cached = 2 * t.splits;
+    t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + 1) / 2, 148 / units})));
     t.smem = tree_tc_smem(p.d_h);
   } else {
   t.pack = rows <= 4;
@@ -532,7 +531,6 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const int64_t tiles = (int64_t(max_pages) * p.page_size + kTile - 1) / kTile;
   const int resident = 148 * (t.nt == 1 ? 2 : 1);
   t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + kWarps - 1) / kWarps, resident / units})));
-  t.cached = t.splits;
   t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
   const int budget = (t.nt == 1 ? 100 : 190) * 1024;
   t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
@@ -543,7 +541,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
   t.smem = std::max(head + std::max(ring, red), draft);
   }
-  t.parts = t.cached + 1;
+  t.parts = t.splits + 1;
   const size_t nrows = size_t(batch) * n_new * n_q;
   t.ws_acc = align_up(sizeof(WsHeader) + nrows * t.parts * sizeof(float2), 256);
   t.ws_total = align_up(t.ws_acc + nrows * t.parts * p.d_h * sizeof(float), 256);
@@ -648,8 +646,7 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   a.n_q = n_q;
   a.gq = n_q / pages->n_kv;
   a.splits = t.splits;
-  a.cached = t.cached;
-  a.parts = k ? t.parts : t.cached;
+  a.parts = k ? t.parts : t.splits;
   a.batch = batch;
   a.blocks = t.blocks;
   a.stages = t.stages;

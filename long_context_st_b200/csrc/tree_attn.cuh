@@ -2,6 +2,9 @@
 #pragma once
 #include "common.cuh"
 #include "pages.cuh"
+#if defined(__CUDACC__)
+#include "sm100.cuh"
+#endif
 
 namespace jolt {
 
@@ -24,7 +27,6 @@ struct TreeArgs {
   int32_t* err;
   float scale2;  // attn_scale * log2(e): scores are kept in log2 units
   int n_new, n_q, gq, splits, parts, batch, blocks, stages, stage_bytes;
-  int cached;  // partial results of the pages (splits, or two a split); the drafted tokens' follows them
 };
 
 // Shared memory of the drafted tokens' part for blocks of `rows` query rows.
@@ -49,6 +51,30 @@ __device__ __forceinline__ uint32_t h2_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 h2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// A warp's bounded wait for an mbarrier phase (false and JOLT_ERR_TIMEOUT after 2 s). A poll asks to be held
+// for up to a millisecond, so that waiting warps leave the issue slots to the others, and the timer (whose
+// read takes longer than most waits here) is read after a poll that came back empty only.
+__device__ __forceinline__ bool wait_all(uint32_t bar, int parity, int32_t* err) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const uint64_t now = sm100::global_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {
+      report_error(err, JOLT_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 // The drafted tokens' own keys and values, in fp32 on the CUDA cores (at most 64 keys).
 template <typename T, int D, int RB, int THREADS>
@@ -111,7 +137,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
       if (lane == 0 && q0 + r < rows) {
         const int row = r0 + q0 + r;
         const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
-        a.ml[gr * a.parts + a.cached] = make_float2(mx, l);
+        a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) o[r][e] = 0.f;
@@ -134,7 +160,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
       if (q0 + r < rows) {
         const int row = r0 + q0 + r;
         const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
-        float* dst = a.acc + (gr * a.parts + a.cached) * D + lane * E;
+        float* dst = a.acc + (gr * a.parts + a.splits) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = o[r][e];
       }
@@ -267,14 +293,14 @@ __device__ void draft_mma(const TreeArgs& a, int b, int h, int r0, uint8_t* smem
       for (int y = 1; y <= 2; y <<= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
       if (r < rows && m == 0) {
         const int64_t gr = (int64_t(b) * a.n_new + i) * a.n_q + h * a.gq + (r0 + r) % a.gq;
-        a.ml[gr * a.parts + a.cached] = make_float2(mx, l);
+        a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
       }
     }
     float* dst[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = rt * 16 + g + 8 * x, row = r0 + r;
-      dst[x] = r < rows ? a.acc + (((int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq) * a.parts + a.cached) * D
+      dst[x] = r < rows ? a.acc + (((int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq) * a.parts + a.splits) * D
                         : nullptr;
     }
 #pragma unroll 2

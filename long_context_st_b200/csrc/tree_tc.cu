@@ -3,16 +3,17 @@
 //
 // A block takes 128 query rows (drafted token x head of the group) of one KV head and a range of the
 // sequence's pages, 128 tokens a tile. Query rows are the MMA's M, so a row's softmax stays with one
-// warp. Even and odd tiles are two streams, each with its own scores and output accumulator in
-// tensor memory, so that one stream's softmax runs under the other's MMAs:
+// warp at a time: two sets of softmax warps take the even and the odd tiles. Tensor memory holds the
+// output (128 columns) and three tiles' scores (128 each), so that the scores of the next two tiles are
+// formed under the softmax of this one:
 //   S = (R q, two f16 terms) x codes^T    A, B from shared memory, K-major
-//   O += P x codes                        A = P (f16) in tensor memory over the scores it came from,
-//                                         B = codes from shared memory, token rows as they are (MN-major)
-// Warps: 0-7 and 8-15 softmax of the two streams (16 rows each), 16-19 widen the keys' codes (global ->
-// registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs. Both code tiles have one layout: a
-// token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8. Features stand in
-// the order in which the widening leaves them; R q is laid out to match, and the outputs are put back
-// at the end.
+//   O += P x values                       A = P (f16) in tensor memory over the scores it came from,
+//                                         B = values from shared memory, token rows as they are (MN-major)
+// Warps: 0-7 and 8-15 softmax of even and odd tiles (16 rows each), 16-19 widen the keys' codes (global ->
+// registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs. Both code tiles have
+// one layout: a token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8.
+// Features stand in the order in which the widening leaves them; R q is laid out to match, and the outputs
+// are put back at the end.
 #include <cuda.h>
 
 #include <algorithm>
@@ -49,13 +50,16 @@ struct Smem {
   static constexpr int q = 0;                      // two terms
   static constexpr int k = q + 2 * kTile;          // two buffers
   static constexpr int v = k + 2 * kTile;          // two buffers
-  static constexpr int sc = v + 2 * kTile;         // [2][64 token pairs][4] floats: key scales, key zeros
-  static constexpr int rs = sc + 2 * 64 * 16;      // [28] warps' largest |R q|
+  static constexpr int sc = v + 2 * kTile;         // [4][64 token pairs][4] floats: key scales, key zeros
+  static constexpr int rs = sc + 4 * 64 * 16;      // [28] warps' largest |R q|; [4] warps' largest values
   static constexpr int qs = rs + 128;              // [128] sum(R q)
-  static constexpr int vis = qs + 512;             // [2][4] words: visible tokens
-  static constexpr int ve = vis + 32;              // [2] value exponent; [2][4] warps' maxima
-  static constexpr int bars = ve + 48;             // 10 mbarriers
-  static constexpr int slot = bars + 80;           // tensor memory base
+  static constexpr int ref = qs + 512;             // [128] the rows' references as the last finished tile left them
+  static constexpr int l = ref + 512;              // [128] the odd tiles' sums
+  static constexpr int vis = l + 512;              // [4][4] words: visible tokens
+  static constexpr int ve = vis + 64;              // [4][2] value exponent of this tile and of the one before
+  static constexpr int red = ve + 32;              // [2][4] warps' largest values
+  static constexpr int bars = red + 32;            // 18 mbarriers
+  static constexpr int slot = bars + 144;          // tensor memory base
   static constexpr int used = slot + 16;
   static constexpr int total = used + 1024;        // swizzled tiles start at 1024-byte boundaries
 };
@@ -219,16 +223,14 @@ struct Ctx {
   uint32_t sb, bar0;
   int n_tiles, tile0, len, h, b;
   float unscale;  // of the scores' accumulators
-  __device__ __forceinline__ uint32_t k_full(int s) const { return bar0 + 8 * s; }
-  __device__ __forceinline__ uint32_t v_full(int s) const { return bar0 + 16 + 8 * s; }
-  __device__ __forceinline__ uint32_t s_done(int s) const { return bar0 + 32 + 8 * s; }
-  __device__ __forceinline__ uint32_t p_full(int s) const { return bar0 + 48 + 8 * s; }
-  __device__ __forceinline__ uint32_t pv_done(int s) const { return bar0 + 64 + 8 * s; }
+  // by tile, four of each (of v_full two): the next use of a barrier can't complete before everyone who waits
+  // for this one has seen it
+  __device__ __forceinline__ uint32_t k_full(int n) const { return bar0 + 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t s_done(int n) const { return bar0 + 32 + 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t p_full(int n) const { return bar0 + 64 + 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t v_full(int n) const { return bar0 + 96 + 8 * (n & 1); }
+  __device__ __forceinline__ uint32_t pv_done(int n) const { return bar0 + 112 + 8 * (n & 3); }
 };
-
-__device__ __forceinline__ bool wait_all(uint32_t bar, int parity, int32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
-}
 
 // Table entries of the two 16-token halves of a warp's 32 tokens, read a tile before they are needed, and
 // the pages they name (-1: past the end, or no page, which is reported).
@@ -283,37 +285,38 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
   int ve = -30;
-  float* red = reinterpret_cast<float*>(c.smem + S::ve + 8);
+  float* red = reinterpret_cast<float*>(c.smem + S::red);
   bool ok = true;
   for (int n = 0; n < c.n_tiles; ++n) {
-    const int s = n & 1, prev = ((n >> 1) & 1) ^ 1;  // parity of the phase that tile n - 2 completed
-    if (n >= 2) ok = ok && wait_all(c.s_done(s), prev, a.err);
+    const int s = n & 1, q = n & 3;
+    if (n >= 2) ok = ok && wait_all(c.s_done(n - 2), ((n - 2) >> 2) & 1, a.err);
     if (ok) widen_keys<D, BK>(w, c.smem + S::k + s * S::kTile, off);
     const float2 kf = __half22float2(ksz), vf = __half22float2(vsz);
     const uint32_t word = __ballot_sync(0xffffffffu, seen);
     const float most = fmaxf(fabsf(vf.y), fabsf(vf.y + vtop * vf.x));
     const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     if (n + 1 < c.n_tiles) fetch(n + 1);
-    // the softmax of tile n - 2 is done with this buffer's scales
-    if (n >= 2) ok = ok && wait_all(c.p_full(s), prev, a.err);
+    // tile n - 4 is done with this place's scales, the widening of its values among it
+    if (n >= 4) ok = ok && wait_all(c.pv_done(n - 4), ((n - 4) >> 2) & 1, a.err);
     if (ok && lane == 0) {
       red[s * 4 + wq] = __uint_as_float(big);
-      reinterpret_cast<uint32_t*>(c.smem + S::vis)[s * 4 + wq] = word;
+      reinterpret_cast<uint32_t*>(c.smem + S::vis)[q * 4 + wq] = word;
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (!ok) continue;
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = fmaxf(top, red[s * 4 + i]);
+    const int before = ve;
     ve = min(max(ve, int(__float_as_uint(top) >> 23) - 126), 30);
     const bool here = (word >> lane) & 1;
-    float* dst = reinterpret_cast<float*>(c.smem + S::sc + s * 1024) + (wq * 16 + (lane >> 1)) * 4 + (lane & 1);
+    float* dst = reinterpret_cast<float*>(c.smem + S::sc + q * 1024) + (wq * 16 + (lane >> 1)) * 4 + (lane & 1);
     dst[0] = here ? kf.x * c.unscale : 0.f;
     dst[2] = here ? kf.y : 0.f;
-    if (wq == 0 && lane == 0) reinterpret_cast<int*>(c.smem + S::ve)[s] = ve;
+    if (wq == 0 && lane == 0) reinterpret_cast<int2*>(c.smem + S::ve)[q] = make_int2(ve, n ? before : ve);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.k_full(s));
+    if (lane == 0) mbar_arrive(c.k_full(n));
   }
 }
 
@@ -344,134 +347,133 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
   for (int n = 0; n < c.n_tiles; ++n) {
-    const int s = n & 1, par = (n >> 1) & 1;
-    if (!wait_all(c.k_full(s), par, a.err)) return;  // ve of this tile
-    const float down = pow2i(kVExp<BV> - reinterpret_cast<const int*>(c.smem + S::ve)[s]);
+    const int s = n & 1;
+    if (!wait_all(c.k_full(n), (n >> 2) & 1, a.err)) return;  // ve of this tile
+    const float down = pow2i(kVExp<BV> - reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3].x);
     float2 sz[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const float2 f = __half22float2(raw[it]);
       sz[it] = make_float2(f.x * down * 16777216.f, f.y * down);
     }
-    if (n >= 2 && !wait_all(c.pv_done(s), par ^ 1, a.err)) return;
+    if (n >= 2 && !wait_all(c.pv_done(n - 2), ((n - 2) >> 2) & 1, a.err)) return;
     widen_values<D, BV>(w, sz, c.smem + S::v + s * S::kTile, off);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.v_full(s));
+    if (lane == 0) mbar_arrive(c.v_full(n));
     if (n + 1 < c.n_tiles) fetch(n + 1);
   }
 }
 
-// Warp 24: scores of tile n, then outputs of tile n - 1.
+// Warp 24: scores of tiles 0 and 1, then of tile n + 2 before the outputs of tile n.
 template <int D>
 __device__ void mma_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int lane) {
   using S = Smem<D>;
   const uint32_t is = idesc_f16(kTok, 0), io = idesc_f16(D, 1);
-  bool ok = true;
-  for (int n = 0; n <= c.n_tiles && ok; ++n) {
-    if (n < c.n_tiles) {
-      const int s = n & 1;
-      ok = wait_all(c.k_full(s), (n >> 1) & 1, a.err);
-      if (!ok) break;
+  // tiles and k-steps differ in the descriptors' start address alone (in 16-byte units, below 2^14)
+  const uint64_t qd = smem_desc_sw128(c.sb + S::q, 16, 1024), kd = smem_desc_sw128(c.sb + S::k, 16, 1024);
+  const uint64_t vd = smem_desc_sw128(c.sb + S::v, S::kChunk, 1024);
+  int buf = 0, pbuf = 0;  // tile % 3
+  for (int n = -2; n < c.n_tiles; ++n) {
+    const int t2 = n + 2;
+    if (t2 < c.n_tiles) {
+      if (!wait_all(c.k_full(t2), (t2 >> 2) & 1, a.err)) return;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t q0 = c.sb + S::q, k0 = c.sb + S::k + s * S::kTile;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = (kk >> 2) * S::kChunk + (kk & 3) * 32;
-            mma_bf16(tmem + s * 128, smem_desc_sw128(q0 + t * S::kTile + at, 16, 1024),
-                     smem_desc_sw128(k0 + at, 16, 1024), is, t + kk > 0);
+            mma_bf16(tmem + 128 + buf * 128, qd + ((t * S::kTile + at) >> 4), kd + (((t2 & 1) * S::kTile + at) >> 4), is,
+                     t + kk > 0);
           }
-        mma_commit(c.s_done(s));
+        mma_commit(c.s_done(t2));
       }
       __syncwarp();
+      buf = buf == 2 ? 0 : buf + 1;
     }
-    if (n >= 1) {
-      const int p = n - 1, s = p & 1;
-      ok = wait_all(c.p_full(s), (p >> 1) & 1, a.err) && wait_all(c.v_full(s), (p >> 1) & 1, a.err);
-      if (!ok) break;
+    if (n >= 0) {
+      if (!wait_all(c.p_full(n), (n >> 2) & 1, a.err) || !wait_all(c.v_full(n), (n >> 1) & 1, a.err)) return;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t v0 = c.sb + S::v + s * S::kTile, pt = tmem + s * 128;
+        const uint64_t vs = vd + (((n & 1) * S::kTile) >> 4);
+        const uint32_t pt = tmem + 128 + pbuf * 128;
 #pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk) {
-          const uint64_t bd = smem_desc_sw128(v0 + kk * 2048, S::kChunk, 1024);
-          const uint32_t at = pt + (kk >> 1) * 32 + (kk & 1) * 8;
-          mma_bf16_tmem_a(tmem + 256 + s * 128, at, bd, io, p >= 2 || kk > 0);
-        }
-        mma_commit(c.pv_done(s));
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          mma_bf16_tmem_a(tmem, pt + (kk >> 1) * 32 + (kk & 1) * 8, vs + ((kk * 2048) >> 4), io, n > 0 || kk > 0);
+        mma_commit(c.pv_done(n));
       }
       __syncwarp();
+      pbuf = pbuf == 2 ? 0 : pbuf + 1;
     }
   }
 }
 
-// Softmax of 16 rows of one stream. Thread (g, m) has rows row0 + g and row0 + g + 8 and the tokens 8j + 2m,
-// 8j + 2m + 1: four lanes share a row, and a token pair's scales serve two rows.
-// With s = scale_k acc + zero_k qs: p = 2^(s - ref + 7). ref is a whole number, 4 above
-// the row's maximum when it was last set. It is set anew only when a thread's eight p of a chunk add up to
-// more than 2^15 (some score then passed it by 5 or more; until then p fits f16), which after a row's first
-// tokens is rare: the usual pass needs no maximum. What was formed under the old reference (this tile's P,
-// the sum, O) is then multiplied by a power of two. That took 8% of the chunks, and a third of the
-// kernel's time, when ref was set to the maximum itself.
+// Softmax of 16 rows in every other tile (strm: even or odd). Thread (g, m) has rows row0 + g and row0 + g + 8
+// and the tokens 8j + 2m, 8j + 2m + 1: four lanes share a row, and a token pair's scales serve two rows.
+// With s = scale_k acc + zero_k qs: p = 2^(s - ref + 7). ref is a whole number, 4 above the row's maximum
+// when it was last set. It is set anew only when a thread's eight p of a chunk add up to more than 2^15
+// (some score then passed it by 5 or more; until then p fits f16), which after a row's first tokens is
+// rare: the usual pass needs no maximum. What was formed under the old reference is then multiplied by a
+// power of two: this tile's P and the sum at once, O at the tile's end, when the two sets of warps also
+// agree: a tile's reference is at least the one that the tile before it ended with.
 template <int D>
 __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int strm, int row0, int lane, int r0,
                              int rows, int split) {
   using S = Smem<D>;
   const int g = lane >> 2, m = lane & 3;
-  const uint32_t ts = tmem + strm * 128 + (uint32_t(row0) << 16);
-  const uint32_t to = tmem + 256 + strm * 128 + (uint32_t(row0) << 16);
+  const uint32_t to = tmem + (uint32_t(row0) << 16);
+  float* const ref_s = reinterpret_cast<float*>(c.smem + S::ref) + row0 + g;
   float ref[2];
   f2 l2[2], qs2[2], neg2[2];  // neg2: 7 - ref; +inf before the first: every p is then too large
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const float qs = reinterpret_cast<const float*>(c.smem + S::qs)[row0 + g + 8 * r];
     qs2[r] = f2_make(qs, qs);
-    neg2[r] = f2_make(INFINITY, INFINITY);
     ref[r] = -INFINITY;
+    neg2[r] = f2_make(INFINITY, INFINITY);
     l2[r] = f2_make(0.f, 0.f);
   }
-  int ve = -30;
-  bool ok = true;
-  // O of these rows times f, after the last product into it (tile n - 2's)
-  auto scale_o = [&](float f0, float f1, int par) {
-    if (!wait_all(c.pv_done(strm), par ^ 1, a.err)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int ch = 0; ch < D / 32; ++ch) {
-      uint32_t x[16];
-      ld_16x256(to + ch * 32, x);
-      ld_wait(x);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * ((i & 2) ? f1 : f0));
-      st_16x256(to + ch * 32, x);
-    }
-    tmem_st_wait();
-    return true;
+  // raises row r's reference to `now` (at least ref): the factor of what was formed under the old one
+  auto raise = [&](int r, float now) {
+    const float f = now == ref[r] ? 1.f : ex2(ref[r] - now);
+    ref[r] = now;
+    neg2[r] = f2_make(kPExp - now, kPExp - now);
+    l2[r] = f2_mul(l2[r], f2_make(f, f));
+    return f;
   };
+  bool ok = true;
   for (int n = strm; n < c.n_tiles; n += 2) {
-    const int par = (n >> 1) & 1;
-    ok = wait_all(c.k_full(strm), par, a.err) && wait_all(c.s_done(strm), par, a.err);
+    const int par = (n >> 2) & 1;
+    ok = wait_all(c.k_full(n), par, a.err) && wait_all(c.s_done(n), par, a.err);
     if (!ok) break;
     tc_fence_after();
-    uint32_t x[16];
-    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(c.smem + S::sc + strm * 1024) + m;
-    const uint32_t* vis = reinterpret_cast<const uint32_t*>(c.smem + S::vis) + strm * 4;
-    const int ve_now = reinterpret_cast<const int*>(c.smem + S::ve)[strm];
-    if (ve_now != ve) {
-      const float drop = pow2i(max(ve - ve_now, -126));
-      ve = ve_now;
-      if (n >= 2) {
-        ok = scale_o(drop, drop, par);
-        if (!ok) break;
-      }
-    }
+    const uint32_t ts = tmem + 128 + (n % 3) * 128 + (uint32_t(row0) << 16);
+    const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(c.smem + S::sc + (n & 3) * 1024) + m;
+    const uint32_t* vis = reinterpret_cast<const uint32_t*>(c.smem + S::vis) + (n & 3) * 4;
+    const int2 ve = reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3];
     const bool whole = (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu;
+    // this tile's P of chunks [0, end) times f
+    auto scale_p = [&](float f0, float f1, int end) {
+      tmem_st_wait();
+#pragma unroll 1
+      for (int e = 0; e < end; ++e) {
+        uint32_t y[8];
+        ld_16x128(ts + e * 32, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn((i & 1) ? f1 : f0));
+          y[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        st_16x128(ts + e * 32, y);
+      }
+    };
     bool tried = false;
 #pragma unroll 1  // one copy of the body: the roles' code together is already long for the instruction cache
     for (int ch = 0; ch < 4;) {
+      uint32_t x[16];
       ld_16x256(ts + ch * 32, x);
       ld_wait(x);
       f2 e2[4][2];
@@ -510,7 +512,7 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
       if (!tried && __any_sync(0xffffffffu, fmaxf(s0.x + s0.y, s1.x + s1.y) > kMost)) {
         // new references, from this chunk's scores read again; then the chunk once more
         tried = true;
-        float top[2] = {-INFINITY, -INFINITY}, f[2];
+        float top[2] = {-INFINITY, -INFINITY};
         ld_16x256(ts + ch * 32, x);
         ld_wait(x);
 #pragma unroll
@@ -525,32 +527,14 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
             if (word & 2) top[r] = fmaxf(top[r], t.y);
           }
         }
+        float f[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-          const float now = fmaxf(ref[r], ceilf(top[r]) + kRoom);
-          f[r] = now == ref[r] ? 1.f : ex2(ref[r] - now);
-          ref[r] = now;
-          l2[r] = f2_mul(l2[r], f2_make(f[r], f[r]));
-          const float neg = kPExp - now;
-          neg2[r] = f2_make(neg, neg);
+          f[r] = raise(r, fmaxf(ref[r], ceilf(top[r]) + kRoom));
         }
-        tmem_st_wait();
-#pragma unroll 1
-        for (int e = 0; e < ch; ++e) {
-          uint32_t y[8];
-          ld_16x128(ts + e * 32, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn(f[i & 1]));
-            y[i] = *reinterpret_cast<const uint32_t*>(&v);
-          }
-          st_16x128(ts + e * 32, y);
-        }
-        if (n >= 2) ok = scale_o(f[0], f[1], par);
-        if (!ok) break;
+        scale_p(f[0], f[1], ch);
         continue;
       }
       tried = false;
@@ -559,40 +543,83 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
       st_16x128(ts + ch * 32, pk);
       ++ch;
     }
-    if (!ok) break;
+    if (n > 0) {
+      // the references that tile n - 1 ended with, and O, which is in their and its values' units
+      ok = wait_all(c.p_full(n - 1), ((n - 1) >> 2) & 1, a.err);
+      if (!ok) break;
+      const float drop = pow2i(max(ve.y - ve.x, -126));
+      float fp[2], fo[2];
+      bool p_too = false, o_too = drop != 1.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float was = ref_s[8 * r];
+        const float now = fmaxf(was, ref[r]);
+        fo[r] = (now == was ? 1.f : ex2(was - now)) * drop;
+        p_too = p_too || now != ref[r];
+        o_too = o_too || now != was;
+        fp[r] = raise(r, now);
+      }
+      if (__any_sync(0xffffffffu, p_too)) scale_p(fp[0], fp[1], 4);
+      if (__any_sync(0xffffffffu, o_too)) {
+        ok = wait_all(c.pv_done(n - 1), ((n - 1) >> 2) & 1, a.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t x[16];
+          ld_16x256(to + ch * 32, x);
+          ld_wait(x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo[(i >> 1) & 1]);
+          st_16x256(to + ch * 32, x);
+        }
+      }
+    }
+    if (m == 0) {
+      ref_s[0] = ref[0];
+      ref_s[8] = ref[1];
+    }
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.p_full(strm));
+    if (lane == 0) mbar_arrive(c.p_full(n));
   }
-  // ---- this stream's partial result ----
-  const int mine = (c.n_tiles - strm + 1) >> 1;  // tiles of the stream
-  if (mine > 0 && ok) {
-    ok = wait_all(c.pv_done(strm), (mine - 1) & 1, a.err);
+  // ---- the block's partial result: the two sets' sums together, half of O's columns each ----
+  const int last = c.n_tiles - 1;
+  if (ok && last >= 0) {
+    ok = wait_all(c.p_full(last), (last >> 2) & 1, a.err) && wait_all(c.pv_done(last), (last >> 2) & 1, a.err);
     tc_fence_after();
   }
-  const float unit = pow2i(ve - (a.p.bv - 10));  // kVExp
+  float l[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (ok && last >= 0) raise(r, fmaxf(ref[r], ref_s[8 * r]));
+    const float2 f = f2_get(l2[r]);
+    l[r] = f.x + f.y;
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+    if (strm == 1 && m == 0) reinterpret_cast<float*>(c.smem + S::l)[row0 + g + 8 * r] = l[r];
+  }
+  asm volatile("bar.sync 2, 512;" ::: "memory");
   float* dst[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const float2 lf = f2_get(l2[r]);
-    float l = lf.x + lf.y;
-#pragma unroll
-    for (int x = 1; x <= 2; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     const int row = row0 + g + 8 * r;
     dst[r] = nullptr;
     if (row < rows) {
       const int q = r0 + row;
       const int64_t gr = (int64_t(c.b) * a.n_new + q / a.gq) * a.n_q + c.h * a.gq + q % a.gq;
-      const int64_t part = gr * a.parts + 2 * split + strm;
-      if (m == 0) a.ml[part] = make_float2(ref[r] - kPExp, l);  // p and O were carried times 2^7
+      const int64_t part = gr * a.parts + split;
+      if (strm == 0 && m == 0)  // p and O were carried times 2^7
+        a.ml[part] = make_float2(ref[r] - kPExp, l[r] + reinterpret_cast<const float*>(c.smem + S::l)[row]);
       if (ref[r] != -INFINITY) dst[r] = a.acc + part * D;
     }
   }
-  if (mine <= 0 || !ok) return;
+  if (last < 0 || !ok) return;
+  const float unit = pow2i(reinterpret_cast<const int2*>(c.smem + S::ve)[last & 3].x - (a.p.bv - 10));  // kVExp
   const int nc = 32 / a.p.bv, hn = nc / 2;
 #pragma unroll 1
-  for (int ch = 0; ch < D / 32; ++ch) {
+  for (int ch = strm * (D / 64); ch < (strm + 1) * (D / 64); ++ch) {
     uint32_t x[16];
     ld_16x256(to + ch * 32, x);
     ld_wait(x);
@@ -640,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   if (warp == 24) {
     tmem_alloc(smem_u32(slot), 512);
     if (lane == 0) {
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(c.k_full(s), 4);
-        mbar_init(c.v_full(s), 4);
-        mbar_init(c.s_done(s), 1);
-        mbar_init(c.p_full(s), 8);
-        mbar_init(c.pv_done(s), 1);
+      for (int n = 0; n < 4; ++n) {
+        mbar_init(c.k_full(n), 4);
+        mbar_init(c.s_done(n), 1);
+        mbar_init(c.p_full(n), 8);
+        if (n < 2) mbar_init(c.v_full(n), 4);
+        mbar_init(c.pv_done(n), 1);
       }
       fence_mbar_init();
     }
