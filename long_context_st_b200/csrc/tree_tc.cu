@@ -10,7 +10,7 @@
 //   O += P x values                       A = P (f16) in tensor memory over the scores it came from,
 //                                         B = values from shared memory, token rows as they are (MN-major)
 // Warps: 0-7 and 8-15 softmax of even and odd tiles (16 rows each), 16-19 widen the keys' codes (global ->
-// registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs. Both code tiles have
+// registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs, 25 prepares the scales. Both code tiles have
 // one layout: a token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8.
 // Features stand in the order in which the widening leaves them; R q is laid out to match, and the outputs
 // are put back at the end.
@@ -27,12 +27,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 896;  // seven warpgroups
+// 26 warps of 72 registers. (A re-split of the registers between the roles, 80 for the softmax and 64 for the
+// widening, made the compiler spill in the widening and cost 10%.)
+constexpr int kThreads = 832;
 constexpr int kRows = 128;   // query rows of a block
 constexpr int kTok = 128;    // tokens of a tile
-// registers a thread after the warpgroups' re-split (launch: 72 each)
-constexpr int kRegLaunch = 72, kRegSoft = 80, kRegWiden = 64, kRegMma = 48;
-static_assert(4 * kRegSoft + 2 * kRegWiden + kRegMma <= 7 * kRegLaunch, "register shares");
 constexpr float kPExp = 7.f;     // p is carried times 2^7
 constexpr float kRoom = 4.f;     // how far above a row's maximum its reference is set
 constexpr float kMost = 32768.f;  // and a thread's sum of eight of them below 2^15, so that each is within f16
@@ -51,15 +50,14 @@ struct Smem {
   static constexpr int k = q + 2 * kTile;          // two buffers
   static constexpr int v = k + 2 * kTile;          // two buffers
   static constexpr int sc = v + 2 * kTile;         // [4][64 token pairs][4] floats: key scales, key zeros
-  static constexpr int rs = sc + 4 * 64 * 16;      // [28] warps' largest |R q|; [4] warps' largest values
+  static constexpr int rs = sc + 4 * 64 * 16;      // [26] warps' largest |R q|
   static constexpr int qs = rs + 128;              // [128] sum(R q)
   static constexpr int ref = qs + 512;             // [128] the rows' references as the last finished tile left them
   static constexpr int l = ref + 512;              // [128] the odd tiles' sums
   static constexpr int vis = l + 512;              // [4][4] words: visible tokens
   static constexpr int ve = vis + 64;              // [4][2] value exponent of this tile and of the one before
-  static constexpr int red = ve + 32;              // [2][4] warps' largest values
-  static constexpr int bars = red + 32;            // 18 mbarriers
-  static constexpr int slot = bars + 144;          // tensor memory base
+  static constexpr int bars = ve + 32;             // 22 mbarriers
+  static constexpr int slot = bars + 176;          // tensor memory base
   static constexpr int used = slot + 16;
   static constexpr int total = used + 1024;        // swizzled tiles start at 1024-byte boundaries
 };
@@ -200,21 +198,14 @@ __device__ __forceinline__ void piece_offsets(int row0, int g, int m, int (&off)
   }
 }
 
-// Raw codes of this warp's 32 token rows in segment seg of their pages (nullptr: zeros).
+// Raw codes of this warp's 32 token rows: two 16-token halves at p0 and p1.
 template <int D, int B>
-__device__ __forceinline__ void load_raw(const PagesDev& p, uint32_t seg, const uint8_t* const (&page)[2], int h, int tok0, int g,
-                                         int m, uint32_t (&w)[4][D * B / 128]) {
-  constexpr int W = D * B / 128;
-  const int ps = 1 << p.ps_log2;
-#pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    if (page[it >> 1]) {
-      load_words<W>(page[it >> 1] + seg + (uint32_t(h) * ps + ((tok0 + it * 8 + g) & (ps - 1))) * uint32_t(D * B / 8) + m * (4 * W), w[it]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[it][i] = 0;
-    }
-  }
+__device__ __forceinline__ void load_raw(const uint8_t* p0, const uint8_t* p1, uint32_t (&w)[4][D * B / 128]) {
+  constexpr int W = D * B / 128, RB = D * B / 8;
+  load_words<W>(p0, w[0]);
+  load_words<W>(p0 + 8 * RB, w[1]);
+  load_words<W>(p1, w[2]);
+  load_words<W>(p1 + 8 * RB, w[3]);
 }
 
 template <int D>
@@ -230,10 +221,11 @@ struct Ctx {
   __device__ __forceinline__ uint32_t p_full(int n) const { return bar0 + 64 + 8 * (n & 3); }
   __device__ __forceinline__ uint32_t v_full(int n) const { return bar0 + 96 + 8 * (n & 1); }
   __device__ __forceinline__ uint32_t pv_done(int n) const { return bar0 + 112 + 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t sc_full(int n) const { return bar0 + 144 + 8 * (n & 3); }
 };
 
-// Table entries of the two 16-token halves of a warp's 32 tokens, read a tile before they are needed, and
-// the pages they name (-1: past the end, or no page, which is reported).
+// The pages of the two 16-token halves of a warp's 32 tokens. Table entries are read a tile before they are
+// needed. A half past the end, or without a page (which is reported), is read from page 0 and not seen.
 template <int D>
 struct Halves {
   int id[2];
@@ -244,18 +236,21 @@ struct Halves {
       if (tok0 + 16 * x < c.len) id[x] = a.p.table[int64_t(c.b) * a.p.max_pages + ((tok0 + 16 * x) >> a.p.ps_log2)];
     }
   }
-  __device__ __forceinline__ const uint8_t* page(const TreeArgs& a, const Ctx<D>& c, int tok0, int x) const {
-    if (uint32_t(id[x]) >= uint32_t(a.p.n_pages)) {
-      if (tok0 + 16 * x < c.len) report_error(a.err, JOLT_ERR_INVALID_ARG);
-      return nullptr;
+  // bit x: half x has a page
+  __device__ __forceinline__ int pages(const TreeArgs& a, const Ctx<D>& c, int tok0, const uint8_t* (&page)[2]) const {
+    int there = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bool ok = uint32_t(id[x]) < uint32_t(a.p.n_pages);
+      there |= int(ok) << x;
+      page[x] = a.p.pool + (ok ? uint64_t(uint32_t(id[x])) * a.p.page_bytes : 0);
+      if (!ok && tok0 + 16 * x < c.len) report_error(a.err, JOLT_ERR_INVALID_ARG);
     }
-    return a.p.pool + uint64_t(uint32_t(id[x])) * a.p.page_bytes;
+    return there;
   }
 };
 
-// Warps 16-19: the keys' codes to f16 tiles, the keys' (scale, zero) per token pair as the softmax uses them,
-// and the exponent of the values' largest magnitude so far (ve): the values are widened in units of 2^(ve - kVExp).
-// After a wait that gave up (reported) a warp only keeps step at the named barrier.
+// Warps 16-19: the keys' codes to f16 tiles.
 template <int D, int BK>
 __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) {
   using S = Smem<D>;
@@ -264,59 +259,86 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   uint32_t w[4][D * BK / 128];
   int off[D / 32];
   piece_offsets<D>(wq * 32, g, m, off);
-  const float vtop = float((1 << a.p.bv) - 1);
-  __half2 ksz, vsz;
-  bool seen;
+  // a tile starts at a page's start (pages have at most 128 tokens), so places in a page stay the same
+  const uint32_t at0 = a.p.kc + (uint32_t(c.h) * ps + ((wq * 32) & (ps - 1)) + g) * uint32_t(D * BK / 8) + m * (D * BK / 32);
+  const uint32_t at1 = at0 + (ps == 16 ? 0 : 16 * (D * BK / 8));
   Halves<D> hv;
   auto fetch = [&](int n) {
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    const uint8_t* const page[2] = {hv.page(a, c, tok0, 0), hv.page(a, c, tok0, 1)};
+    const uint8_t* page[2];
+    hv.pages(a, c, tok0, page);
     hv.read(a, c, tok0 + kTok);
-    load_raw<D, BK>(a.p, a.p.kc, page, c.h, tok0, g, m, w);
-    const uint8_t* base = lane < 16 ? page[0] : page[1];  // the lane's own token
-    seen = base && tok0 + lane < c.len;
-    ksz = vsz = __floats2half2_rn(0.f, 0.f);
-    if (seen) {
-      const uint32_t row = uint32_t(c.h) * ps + ((tok0 + lane) & (ps - 1));
-      ksz = reinterpret_cast<const __half2*>(base + a.p.ks)[row];
-      vsz = reinterpret_cast<const __half2*>(base + a.p.vs)[row];
-    }
+    load_raw<D, BK>(page[0] + at0, page[1] + at1, w);
   };
   hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
-  int ve = -30;
-  float* red = reinterpret_cast<float*>(c.smem + S::red);
-  bool ok = true;
   for (int n = 0; n < c.n_tiles; ++n) {
-    const int s = n & 1, q = n & 3;
-    if (n >= 2) ok = ok && wait_all(c.s_done(n - 2), ((n - 2) >> 2) & 1, a.err);
-    if (ok) widen_keys<D, BK>(w, c.smem + S::k + s * S::kTile, off);
-    const float2 kf = __half22float2(ksz), vf = __half22float2(vsz);
-    const uint32_t word = __ballot_sync(0xffffffffu, seen);
-    const float most = fmaxf(fabsf(vf.y), fabsf(vf.y + vtop * vf.x));
-    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-    if (n + 1 < c.n_tiles) fetch(n + 1);
-    // tile n - 4 is done with this place's scales, the widening of its values among it
-    if (n >= 4) ok = ok && wait_all(c.pv_done(n - 4), ((n - 4) >> 2) & 1, a.err);
-    if (ok && lane == 0) {
-      red[s * 4 + wq] = __uint_as_float(big);
-      reinterpret_cast<uint32_t*>(c.smem + S::vis)[q * 4 + wq] = word;
-    }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (!ok) continue;
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, red[s * 4 + i]);
-    const int before = ve;
-    ve = min(max(ve, int(__float_as_uint(top) >> 23) - 126), 30);
-    const bool here = (word >> lane) & 1;
-    float* dst = reinterpret_cast<float*>(c.smem + S::sc + q * 1024) + (wq * 16 + (lane >> 1)) * 4 + (lane & 1);
-    dst[0] = here ? kf.x * c.unscale : 0.f;
-    dst[2] = here ? kf.y : 0.f;
-    if (wq == 0 && lane == 0) reinterpret_cast<int2*>(c.smem + S::ve)[q] = make_int2(ve, n ? before : ve);
+    if (n >= 2 && !wait_all(c.s_done(n - 2), ((n - 2) >> 2) & 1, a.err)) return;
+    widen_keys<D, BK>(w, c.smem + S::k + (n & 1) * S::kTile, off);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.k_full(n));
+    if (n + 1 < c.n_tiles) fetch(n + 1);
+  }
+}
+
+// Warp 25: per token pair the keys' (scale, zero) as the softmax uses them, which tokens are seen, and the
+// exponent of the values' largest magnitude so far (ve): values are widened in units of 2^(ve - kVExp).
+// Four tokens a lane.
+template <int D>
+__device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
+  using S = Smem<D>;
+  const int ps = 1 << a.p.ps_log2;
+  const float vtop = float((1 << a.p.bv) - 1);
+  const uint32_t at = (uint32_t(c.h) * ps + ((lane * 4) & (ps - 1))) * 4;
+  int id = -1, seen = 0;
+  uint4 kz, vz;
+  auto entry = [&](int n) {
+    const int tok = (c.tile0 + n) * kTok + lane * 4;
+    id = tok < c.len ? a.p.table[int64_t(c.b) * a.p.max_pages + (tok >> a.p.ps_log2)] : -1;
+  };
+  auto fetch = [&](int n) {
+    const int tok = (c.tile0 + n) * kTok + lane * 4;
+    const bool ok = uint32_t(id) < uint32_t(a.p.n_pages);
+    if (!ok && tok < c.len) report_error(a.err, JOLT_ERR_INVALID_ARG);
+    seen = ok ? (1 << min(max(c.len - tok, 0), 4)) - 1 : 0;
+    const uint8_t* base = a.p.pool + (ok ? uint64_t(uint32_t(id)) * a.p.page_bytes : 0) + at;
+    entry(n + 1);
+    kz = *reinterpret_cast<const uint4*>(base + a.p.ks);
+    vz = *reinterpret_cast<const uint4*>(base + a.p.vs);
+  };
+  entry(0);
+  fetch(0);
+  int ve = -30;
+  for (int n = 0; n < c.n_tiles; ++n) {
+    const int q = n & 3;
+    // tile n - 4 is done with this place, the widening of its values among it
+    if (n >= 4 && !wait_all(c.pv_done(n - 4), ((n - 4) >> 2) & 1, a.err)) return;
+    const uint32_t ku[4] = {kz.x, kz.y, kz.z, kz.w}, vu[4] = {vz.x, vz.y, vz.z, vz.w};
+    float sc[4], ze[4], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 k = h2_floats(ku[i]), v = h2_floats(vu[i]);
+      const bool here = (seen >> i) & 1;
+      sc[i] = here ? k.x * c.unscale : 0.f;
+      ze[i] = here ? k.y : 0.f;
+      if (here) most = fmaxf(most, fmaxf(fabsf(v.y), fabsf(v.y + vtop * v.x)));
+    }
+    float4* dst = reinterpret_cast<float4*>(c.smem + S::sc + q * 1024) + lane * 2;
+    dst[0] = make_float4(sc[0], sc[1], ze[0], ze[1]);
+    dst[1] = make_float4(sc[2], sc[3], ze[2], ze[3]);
+    // eight lanes' four tokens a word
+    uint32_t word = uint32_t(seen) << (4 * (lane & 7));
+#pragma unroll
+    for (int x = 1; x <= 4; x <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, x);
+    if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(c.smem + S::vis)[q * 4 + (lane >> 3)] = word;
+    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    const int before = ve;
+    ve = min(max(ve, int(big >> 23) - 126), 30);
+    if (lane == 0) reinterpret_cast<int2*>(c.smem + S::ve)[q] = make_int2(ve, n ? before : ve);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.sc_full(n));
+    if (n + 1 < c.n_tiles) fetch(n + 1);
   }
 }
 
@@ -330,31 +352,36 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   __half2 raw[4];
   int off[D / 32];
   piece_offsets<D>(wq * 32, g, m, off);
+  const uint32_t head = uint32_t(c.h) * ps, in_page = ((wq * 32) & (ps - 1)) + g;
+  const uint32_t at0 = a.p.vc + (head + in_page) * uint32_t(D * BV / 8) + m * (D * BV / 32);
+  const uint32_t at1 = at0 + (ps == 16 ? 0 : 16 * (D * BV / 8));
+  const uint32_t sz0 = a.p.vs + (head + in_page) * 4, sz1 = sz0 + (ps == 16 ? 0 : 64);
   Halves<D> hv;
+  int seen;  // bit it: the lane's row of group it
   auto fetch = [&](int n) {
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    const uint8_t* const page[2] = {hv.page(a, c, tok0, 0), hv.page(a, c, tok0, 1)};
+    const uint8_t* page[2];
+    const int there = hv.pages(a, c, tok0, page);
     hv.read(a, c, tok0 + kTok);
+    seen = 0;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const int tok = tok0 + it * 8 + g;
-      raw[it] = __floats2half2_rn(0.f, 0.f);
-      if (page[it >> 1] && tok < c.len)
-        raw[it] = reinterpret_cast<const __half2*>(page[it >> 1] + a.p.vs)[uint32_t(c.h) * ps + (tok & (ps - 1))];
+      seen |= int(((there >> (it >> 1)) & 1) && tok0 + it * 8 + g < c.len) << it;
+      raw[it] = *reinterpret_cast<const __half2*>(page[it >> 1] + (it < 2 ? sz0 : sz1) + (it & 1) * 32);
     }
-    load_raw<D, BV>(a.p, a.p.vc, page, c.h, tok0, g, m, w);
+    load_raw<D, BV>(page[0] + at0, page[1] + at1, w);
   };
   hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
   for (int n = 0; n < c.n_tiles; ++n) {
     const int s = n & 1;
-    if (!wait_all(c.k_full(n), (n >> 2) & 1, a.err)) return;  // ve of this tile
+    if (!wait_all(c.sc_full(n), (n >> 2) & 1, a.err)) return;  // ve of this tile
     const float down = pow2i(kVExp<BV> - reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3].x);
     float2 sz[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const float2 f = __half22float2(raw[it]);
-      sz[it] = make_float2(f.x * down * 16777216.f, f.y * down);
+      sz[it] = (seen >> it) & 1 ? make_float2(f.x * (down * 16777216.f), f.y * down) : make_float2(0.f, 0.f);
     }
     if (n >= 2 && !wait_all(c.pv_done(n - 2), ((n - 2) >> 2) & 1, a.err)) return;
     widen_values<D, BV>(w, sz, c.smem + S::v + s * S::kTile, off);
@@ -446,7 +473,7 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
   bool ok = true;
   for (int n = strm; n < c.n_tiles; n += 2) {
     const int par = (n >> 2) & 1;
-    ok = wait_all(c.k_full(n), par, a.err) && wait_all(c.s_done(n), par, a.err);
+    ok = wait_all(c.sc_full(n), par, a.err) && wait_all(c.s_done(n), par, a.err);
     if (!ok) break;
     tc_fence_after();
     const uint32_t ts = tmem + 128 + (n % 3) * 128 + (uint32_t(row0) << 16);
@@ -673,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
         mbar_init(c.p_full(n), 8);
         if (n < 2) mbar_init(c.v_full(n), 4);
         mbar_init(c.pv_done(n), 1);
+        mbar_init(c.sc_full(n), 1);
       }
       fence_mbar_init();
     }
@@ -746,11 +774,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   tc_fence_after();
   const uint32_t tmem = *slot;
   if (warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoft));
     // a warp reaches the 32 lanes of its quarter, warp % 4
     softmax_role<D>(a, c, tmem, warp >> 3, (warp & 3) * 32 + ((warp >> 2) & 1) * 16, lane, r0, rows, split);
   } else if (warp < 24) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWiden));
     if (c.n_tiles > 0) {
       const int bits = warp < 20 ? a.p.bk : a.p.bv;
       if (warp < 20) {
@@ -764,8 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
     if (warp == 24) mma_role<D>(a, c, tmem, lane);
+    if (warp == 25 && c.n_tiles > 0) scales_role<D>(a, c, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -777,14 +803,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
 
 template <int D>
 jolt_status launch(const TreeArgs& a, bool draft, size_t smem, cudaStream_t st) {
-  // the warpgroups re-split the block's registers (setmaxnreg): what they take must not pass what the
-  // launch gives, which this build's register count decides
-  static const cudaError_t fits = [] {
-    cudaFuncAttributes at;
-    const cudaError_t e = cudaFuncGetAttributes(&at, k_tree_tc<D>);
-    return e != cudaSuccess ? e : at.numRegs == kRegLaunch ? cudaSuccess : cudaErrorInvalidConfiguration;
-  }();
-  JOLT_CUDA_TRY(fits);
   JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
   const dim3 grid(a.splits + (draft ? 1 : 0), a.p.n_kv * a.blocks, a.batch);
   k_tree_tc<D><<<grid, kThreads, smem, st>>>(a, draft ? 1 : 0);
