@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, m = lane & 3;
-  const int h = blockIdx.y / a.blocks, r0 = (blockIdx.y % a.blocks) * RB, b = blockIdx.z;
-  const int split = blockIdx.x;
+  const Work wk = work_of(a);
+  const int h = wk.h, r0 = wk.block * RB, b = wk.b, split = wk.split;
   if (split == a.splits) {
     draft_part<T, D, RB, kThreads>(a, b, h, r0, smem);
     return;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
       for (int e = 0; e < E; ++e) v[e] = 0.f;
       if (r < rows) {
         const int row = r0 + r;
-        const T* x = qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + lane * E;
+        const T* x = qb + q_offset(a, row, D) + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = ld_as_float(x, e) * a.scale2;
       }
@@ -430,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         zs += xz[w * C + col];
       }
       const int row = r0 + col;
-      const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
-      const int64_t part = gr * a.parts + split;
+      const int64_t part = out_row(a, b, h, row) * a.parts + split;
       if (g == 0) a.ml[part] = make_float2(mx[nt][c], ls);
       if (mx[nt][c] == -INFINITY) continue;
       float* dst = a.acc + part * D + g * (D / 8);
@@ -482,6 +481,15 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(s) * D + e];
     }
+  }
+  if (a.perm) {
+    __shared__ float row_s[4][D];
+    float* rs = row_s[threadIdx.x >> 5];
+#pragma unroll
+    for (int e = 0; e < E; ++e) rs[lane * E + e] = o[e];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = rs[place_of(lane * E + e, log2_codes(a.perm), D)];
   }
   warp_fwht<E>(o);
 #pragma unroll
@@ -571,7 +579,7 @@ jolt_status launch_merge(const TreeArgs& a, bool draft, cudaStream_t st) {
 template <typename T, int D, int NT, bool PACK>
 jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
   JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree<T, D, NT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(t.smem)));
-  const dim3 grid(t.splits + (draft ? 1 : 0), a.p.n_kv * t.blocks, a.batch);
+  const unsigned grid = unsigned(t.splits + (draft ? 1 : 0)) * a.p.n_kv * t.blocks * a.batch;
   k_tree<T, D, NT, PACK><<<grid, kThreads, t.smem, st>>>(a);
   JOLT_CUDA_TRY(cudaGetLastError());
   return launch_merge<T, D>(a, draft, st);
@@ -620,7 +628,7 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   if (!rows_ok(q, q_stride_b, q_stride_t) || (!k != !v) || (!prefix_out != !prefix_lse)) return JOLT_ERR_INVALID_ARG;
   if (k && (!rows_ok(k, kv_stride_b, kv_stride_t) || !rows_ok(v, kv_stride_b, kv_stride_t))) return JOLT_ERR_INVALID_ARG;
   const TreePlan t = tree_plan(*pages, batch, n_new, n_q, max_pages);
-  if (int64_t(pages->n_kv) * t.blocks > 65535) return JOLT_ERR_INVALID_ARG;
+  if (int64_t(batch) * pages->n_kv * t.blocks * (t.splits + 1) > (1 << 30)) return JOLT_ERR_INVALID_ARG;
   if (ws_bytes < t.ws_total) return JOLT_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(ws);
   TreeArgs a{};
@@ -645,6 +653,8 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   a.n_new = n_new;
   a.n_q = n_q;
   a.gq = n_q / pages->n_kv;
+  a.gq_magic = uint32_t(((uint64_t(1) << 32) + a.gq - 1) / a.gq);
+  a.perm = t.tc ? pages->b_v : 0;
   a.splits = t.splits;
   a.parts = k ? t.parts : t.splits;
   a.batch = batch;

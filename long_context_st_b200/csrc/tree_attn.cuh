@@ -27,6 +27,8 @@ struct TreeArgs {
   int32_t* err;
   float scale2;  // attn_scale * log2(e): scores are kept in log2 units
   int n_new, n_q, gq, splits, parts, batch, blocks, stages, stage_bytes;
+  uint32_t gq_magic;  // ceil(2^32 / gq)
+  int perm;           // features of acc are in tree_tc.cu's order for this many value bits (0: their own order)
 };
 
 // Shared memory of the drafted tokens' part for blocks of `rows` query rows.
@@ -39,6 +41,42 @@ inline size_t draft_smem(int d_h, int rows, int threads) {
 #if defined(__CUDACC__)
 __device__ __forceinline__ int draft_count(const TreeArgs& a, int b) {
   return a.counts ? min(max(a.counts[b], 0), a.n_new) : a.n_new;
+}
+// Drafted token and head of the group of a query row.
+__device__ __forceinline__ int row_token(const TreeArgs& a, int row) {
+  return a.gq == 1 ? row : int(__umulhi(uint32_t(row), a.gq_magic));
+}
+// Element offset of a row from its KV head's first query row.
+__device__ __forceinline__ int64_t q_offset(const TreeArgs& a, int row, int d) {
+  const int t = row_token(a, row);
+  return int64_t(t) * a.qst + (row - t * a.gq) * d;
+}
+// Row of out, lse, ml and acc.
+__device__ __forceinline__ int64_t out_row(const TreeArgs& a, int b, int h, int row) {
+  const int t = row_token(a, row);
+  return (int64_t(b) * a.n_new + t) * a.n_q + h * a.gq + (row - t * a.gq);
+}
+// What a block works on: the pages' splits of all (sequence, KV head, row block) first, then the drafted
+// tokens' parts (split == splits), which are short and fill the SMs that the splits leave.
+struct Work {
+  int b, h, block, split;
+};
+__device__ __forceinline__ Work work_of(const TreeArgs& a) {
+  const int units = a.batch * a.p.n_kv * a.blocks;
+  int id = blockIdx.x, split = a.splits;
+  if (id < units * a.splits) {
+    split = id % a.splits;
+    id /= a.splits;
+  } else {
+    id -= units * a.splits;
+  }
+  Work w;
+  w.block = id % a.blocks;
+  id /= a.blocks;
+  w.h = id % a.p.n_kv;
+  w.b = id / a.p.n_kv;
+  w.split = split;
+  return w;
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 __device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
@@ -98,7 +136,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
   const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
   for (int i = tid; i < rows * D; i += THREADS) {
     const int r = r0 + i / D, f = i % D;
-    qs[i] = ld_as_float(qb, int64_t(r / a.gq) * a.qst + (r % a.gq) * D + f) * a.scale2;
+    qs[i] = ld_as_float(qb, q_offset(a, r, D) + f) * a.scale2;
   }
   __syncthreads();
   for (int q0 = warp * 4; q0 < rows; q0 += (THREADS / 32) * 4) {
@@ -106,7 +144,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
     float s[4][2];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = (r0 + q0 + r) / a.gq;
+      const int i = row_token(a, r0 + q0 + r);
       bits[r] = 0;
       if (q0 + r < rows) bits[r] = a.mask ? a.mask[int64_t(b) * a.n_new + i] : ~uint64_t(0) >> (63 - i);
       if (cnt < 64) bits[r] &= (uint64_t(1) << cnt) - 1;
@@ -136,7 +174,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
       ps[(warp * 4 + r) * 64 + lane + 32] = p2;
       if (lane == 0 && q0 + r < rows) {
         const int row = r0 + q0 + r;
-        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
+        const int64_t gr = out_row(a, b, h, row);
         a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
       }
 #pragma unroll
@@ -159,7 +197,7 @@ __device__ void draft_block(const TreeArgs& a, int b, int h, int r0, uint8_t* sm
     for (int r = 0; r < 4; ++r)
       if (q0 + r < rows) {
         const int row = r0 + q0 + r;
-        const int64_t gr = (int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq;
+        const int64_t gr = out_row(a, b, h, row);
         float* dst = a.acc + (gr * a.parts + a.splits) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = o[r][e];
@@ -230,7 +268,7 @@ __device__ void draft_mma(const TreeArgs& a, int b, int h, int r0, uint8_t* smem
   for (int i = tid; i < tiles * 16 * V; i += THREADS) {
     const int r = i / V, f = (i % V) * 8, row = r0 + r;
     uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows) x = *reinterpret_cast<const uint4*>(qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + f);
+    if (r < rows) x = *reinterpret_cast<const uint4*>(qb + q_offset(a, row, D) + f);
     *reinterpret_cast<uint4*>(qs + r * LD + f) = x;
   }
   __syncthreads();
@@ -258,7 +296,7 @@ __device__ void draft_mma(const TreeArgs& a, int b, int h, int r0, uint8_t* smem
     uint64_t extra[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {  // rows g and g + 8
-      const int r = rt * 16 + g + 8 * x, i = (r0 + r) / a.gq;
+      const int r = rt * 16 + g + 8 * x, i = row_token(a, r0 + r);
       uint64_t bits = 0;
       if (r < rows) bits = a.mask ? a.mask[int64_t(b) * a.n_new + i] : ~uint64_t(0) >> (63 - i);
       if (cnt < 64) bits &= (uint64_t(1) << cnt) - 1;
@@ -292,15 +330,14 @@ __device__ void draft_mma(const TreeArgs& a, int b, int h, int r0, uint8_t* smem
 #pragma unroll
       for (int y = 1; y <= 2; y <<= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
       if (r < rows && m == 0) {
-        const int64_t gr = (int64_t(b) * a.n_new + i) * a.n_q + h * a.gq + (r0 + r) % a.gq;
-        a.ml[gr * a.parts + a.splits] = make_float2(mx, l);
+        a.ml[out_row(a, b, h, r0 + r) * a.parts + a.splits] = make_float2(mx, l);
       }
     }
     float* dst[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = rt * 16 + g + 8 * x, row = r0 + r;
-      dst[x] = r < rows ? a.acc + (((int64_t(b) * a.n_new + row / a.gq) * a.n_q + h * a.gq + row % a.gq) * a.parts + a.splits) * D
+      dst[x] = r < rows ? a.acc + (out_row(a, b, h, row) * a.parts + a.splits) * D
                         : nullptr;
     }
 #pragma unroll 2
@@ -348,6 +385,16 @@ __device__ __forceinline__ void draft_part(const TreeArgs& a, int b, int h, int 
 
 // The form for bf16 and more than 32 query rows a KV head (tree_tc.cu).
 size_t tree_tc_smem(int d_h);
+// Place of feature f in a row of that form's code tiles (in elements) when its codes have 2^lnc a word:
+// quarter row m, piece i of it (pairs 4i .. 4i+3 of code_pair's order), at piece i * 4 + m.
+#if defined(__CUDACC__)
+__device__ __forceinline__ int place_of(int f, int lnc, int D) {
+  const int m = f / (D / 4), fq = f % (D / 4), half = 1 << (lnc - 1);
+  const int c = fq & (2 * half - 1), pair = ((fq >> lnc) << (lnc - 1)) + (c & (half - 1));
+  return ((pair >> 2) * 4 + m) * 8 + (pair & 3) * 2 + (c >> (lnc - 1));
+}
+__device__ __forceinline__ int log2_codes(int bits) { return bits == 2 ? 4 : bits == 4 ? 3 : 2; }
+#endif
 jolt_status launch_tree_tc(const TreeArgs& a, int d_h, bool draft, size_t smem, cudaStream_t st);
 
 }  // namespace jolt

@@ -12,8 +12,8 @@
 // Warps: 0-7 and 8-15 softmax of even and odd tiles (16 rows each), 16-19 widen the keys' codes (global ->
 // registers -> f16 tiles in shared memory), 20-23 the values', 24 issues the MMAs, 25 prepares the scales. Both code tiles have
 // one layout: a token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8.
-// Features stand in the order in which the widening leaves them; R q is laid out to match, and the outputs
-// are put back at the end.
+// Features stand in the order in which the widening leaves them; R q is laid out to match, and the merge puts
+// the outputs back.
 #include <cuda.h>
 
 #include <algorithm>
@@ -133,14 +133,6 @@ __device__ __forceinline__ void ld_wait(uint32_t (&x)[16]) {
                : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]), "+r"(x[8]),
                  "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
                :: "memory");
-}
-
-// Place of feature f in a code tile's row (in elements) when its codes have nc = 32 / b a word: quarter
-// row m, piece i of it (pairs 4i .. 4i+3 of code_pair's order), at piece i * 4 + m.
-__device__ __forceinline__ int place_of(int f, int nc, int D) {
-  const int m = f / (D / 4), fq = f % (D / 4);
-  const int c = fq % nc, pair = (fq / nc) * (nc / 2) + c % (nc / 2);
-  return ((pair >> 2) * 4 + m) * 8 + (pair & 3) * 2 + c / (nc / 2);
 }
 
 // The widening warps hold a token row in four lanes, lane = 8 m + g: row it*8 + g, quarter m. The eight lanes of
@@ -634,9 +626,7 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
     const int row = row0 + g + 8 * r;
     dst[r] = nullptr;
     if (row < rows) {
-      const int q = r0 + row;
-      const int64_t gr = (int64_t(c.b) * a.n_new + q / a.gq) * a.n_q + c.h * a.gq + q % a.gq;
-      const int64_t part = gr * a.parts + split;
+      const int64_t part = out_row(a, c.b, c.h, r0 + row) * a.parts + split;
       if (strm == 0 && m == 0)  // p and O were carried times 2^7
         a.ml[part] = make_float2(ref[r] - kPExp, l[r] + reinterpret_cast<const float*>(c.smem + S::l)[row]);
       if (ref[r] != -INFINITY) dst[r] = a.acc + part * D;
@@ -644,40 +634,37 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
   }
   if (last < 0 || !ok) return;
   const float unit = pow2i(reinterpret_cast<const int2*>(c.smem + S::ve)[last & 3].x - (a.p.bv - 10));  // kVExp
-  const int nc = 32 / a.p.bv, hn = nc / 2;
+  // in the tiles' order of features: the merge puts the sum over the splits into their own
 #pragma unroll 1
   for (int ch = strm * (D / 64); ch < (strm + 1) * (D / 64); ++ch) {
     uint32_t x[16];
     ld_16x256(to + ch * 32, x);
     ld_wait(x);
-    const int pair = ch * 4 + m;  // piece ch * 4 + at: quarter row `at`, pairs 4 ch ..
 #pragma unroll
-    for (int at = 0; at < 4; ++at) {
-      const int f = at * (D / 4) + (pair / hn) * nc + pair % hn;
+    for (int at = 0; at < 4; ++at)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (dst[r]) {
-          dst[r][f] = __uint_as_float(x[4 * at + 2 * r]) * unit;
-          dst[r][f + hn] = __uint_as_float(x[4 * at + 2 * r + 1]) * unit;
-        }
-    }
+        if (dst[r])
+          *reinterpret_cast<float2*>(dst[r] + ch * 32 + at * 8 + 2 * m) =
+              make_float2(__uint_as_float(x[4 * at + 2 * r]) * unit, __uint_as_float(x[4 * at + 2 * r + 1]) * unit);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int draft_x) {
+__global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
   using S = Smem<D>;
   constexpr int E = D / 32;
   extern __shared__ uint8_t raw[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y / a.blocks, r0 = (blockIdx.y % a.blocks) * kRows, b = blockIdx.z;
-  const int split = int(blockIdx.x) - draft_x;  // the drafted tokens' blocks come first: they are short
+  const Work wk = work_of(a);
+  const int h = wk.h, r0 = wk.block * kRows, b = wk.b, split = wk.split;
   uint8_t* smem = align_smem_1024(raw);
-  if (split < 0) {
+  if (split == a.splits) {
     draft_part<__nv_bfloat16, D, kRows, kThreads>(a, b, h, r0, smem);
     return;
   }
+  const int len = pages_len(a.p, b, a.err);  // read with the count, not after it
   const int rows = min(kRows, draft_count(a, b) * a.gq - r0);
   if (rows <= 0) return;
   Ctx<D> c;
@@ -686,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   c.bar0 = c.sb + S::bars;
   c.h = h;
   c.b = b;
-  c.len = pages_len(a.p, b, a.err);
+  c.len = len;
   const int tiles = (c.len + kTok - 1) / kTok, per = (tiles + a.splits - 1) / a.splits;
   c.tile0 = split * per;
   c.n_tiles = max(0, min(tiles, c.tile0 + per) - c.tile0);
@@ -711,39 +698,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
   {
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
     const float isd = rsqrtf(float(D));
-    const int nc = 32 / a.p.bk;
-    int at[E];
-    float sign[E], low[E];  // low: 2^-(a code field's place in its byte)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      at[e] = place_of(lane * E + e, nc, D);
-      sign[e] = rot_sign(a.p.seed, lane * E + e);
-      low[e] = pow2i(-a.p.bk * (((at[e] & 7) >> 1) % (8 / a.p.bk)));
-    }
     constexpr int kW = kThreads / 32, kPer = (kRows + kW - 1) / kW;
     float v[kPer][E], top = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = warp + i * kW;
+      uint32_t w[E / 2];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-      if (r < rows) {
-        const int row = r0 + r;
-        const __nv_bfloat16* x = qb + int64_t(row / a.gq) * a.qst + (row % a.gq) * D + lane * E;
+      for (int e = 0; e < E / 2; ++e) w[e] = 0;
+      if (r < rows) load_words<E / 2>(reinterpret_cast<const uint8_t*>(qb + q_offset(a, r0 + r, D) + lane * E), w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[i][e] = ld_as_float(x, e) * a.scale2 * sign[e];
-      }
+      for (int e = 0; e < E; ++e) v[i][e] = __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    }
+    int at[E];
+    float sign[E], low[E];  // low: 2^-(a code field's place in its byte)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      at[e] = place_of(lane * E + e, log2_codes(a.p.bk), D);
+      sign[e] = rot_sign(a.p.seed, lane * E + e) * a.scale2;
+      low[e] = pow2i(-(a.p.bk * ((at[e] & 7) >> 1) & 7));  // b (pair % (8 / b)) = (b pair) % 8
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = warp + i * kW;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] *= sign[e];
+      // the elements of H x add up to D x_0
+      if (lane == 0 && r < kRows) reinterpret_cast<float*>(smem + S::qs)[r] = v[i][0] * (float(D) * isd);
       warp_fwht<E>(v[i]);
-      float sum = 0.f, most = 0.f;
+      float most = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         v[i][e] *= isd;
         most = fmaxf(most, fabsf(v[i][e]));
-        sum += v[i][e];
       }
       if (most < INFINITY) top = fmaxf(top, most);  // a row that is not finite is on its own
-      sum = warp_sum(sum);
-      if (lane == 0 && r < kRows) reinterpret_cast<float*>(smem + S::qs)[r] = sum;
     }
     top = warp_max(top);
     if (lane == 0) reinterpret_cast<float*>(smem + S::rs)[warp] = top;
@@ -804,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a, int d
 template <int D>
 jolt_status launch(const TreeArgs& a, bool draft, size_t smem, cudaStream_t st) {
   JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-  const dim3 grid(a.splits + (draft ? 1 : 0), a.p.n_kv * a.blocks, a.batch);
-  k_tree_tc<D><<<grid, kThreads, smem, st>>>(a, draft ? 1 : 0);
+  const unsigned grid = unsigned(a.splits + (draft ? 1 : 0)) * a.p.n_kv * a.blocks * a.batch;
+  k_tree_tc<D><<<grid, kThreads, smem, st>>>(a);
   JOLT_CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
 }
