@@ -60,4 +60,19 @@ __device__ __forceinline__ uint32_t code_across(const uint32_t (&x)[W], const ui
   return centred<B>(bytes_xy(x[bit / 32], y[bit / 32], (bit % 32) / 8), (bit % 8) / B);
 }
 
+// The fields themselves: whole numbers c 2^-24 as f16 bits (subnormals), times 2^(a field's place in its byte).
+template <int B, int W>
+__device__ __forceinline__ uint32_t field_pair(const uint32_t (&w)[W], int i) {
+  constexpr int H = 16 / B, F = 8 / B;  // pairs a word, fields a byte
+  const int p = i % H;
+  const uint32_t x = p >= F ? w[i / H] >> 8 : w[i / H];
+  return x & (0x00010001u * (((1u << B) - 1) << (B * (p % F))));
+}
+// Field `j` of the rows held in x and y, as the pair (x_j, y_j).
+template <int B, int W>
+__device__ __forceinline__ uint32_t field_across(const uint32_t (&x)[W], const uint32_t (&y)[W], int j) {
+  const int bit = j * B;
+  return bytes_xy(x[bit / 32], y[bit / 32], (bit % 32) / 8) & (0x00010001u * (((1u << B) - 1) << (bit % 8)));
+}
+
 }  // namespace jolt

@@ -6,11 +6,14 @@
 // The same for values: sum_t p_t y_t = sum_t (p_t scale_t) (c_t - o) + sum_t p_t (zero_t + o scale_t),
 // whose second term is one number for all features; R^T is applied once, to the sum.
 //
-// Codes are exact in f16, so they feed m16n8k16 MMAs straight from their bits; what is rounded is
-// the other operand: R q is carried as two f16 terms (22 bits: the log-sum-exp stays fp32-accurate),
-// p * scale as one f16 term for bf16 output (11 bits, against the 8 the output keeps) and as two for
-// fp32. Both are first scaled by powers of two into f16's normal range: R q by its row's largest
-// element, p * scale by the largest value scale met so far.
+// A code's field is a whole number c 2^-24 as the bits of an f16 (a subnormal; its place in the byte a
+// further power of two), so codes feed m16n8k16 MMAs after one mask a pair. The places' powers are taken
+// from R q (keys) and from the outputs (values); o and the zeros enter through sums: o sum(R q) in the
+// scores, and for the values a further MMA row of ones, which adds up p * scale exactly as rounded.
+// What is rounded is the other operand: R q is carried as two f16 terms (22 bits: the log-sum-exp stays
+// fp32-accurate), p * scale as one f16 term for bf16 output (11 bits, against the 8 the output keeps) and
+// as two for fp32. Both are first scaled by powers of two into f16's normal range: R q by the block's
+// largest element, p * scale by the largest value scale met so far.
 #include <cuda.h>
 
 #include <algorithm>
@@ -27,8 +30,11 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // tokens a warp takes at a time
 constexpr int kMaxSplits = 63;   // + the drafted tokens' own partial: two per lane in the merge
 constexpr int kMaxStages = 4;
+constexpr float kRoom = 4.f;    // how far above a row's maximum its reference is set
+constexpr float kMost = 256.f;  // most that a thread's p of a tile may add up to
+constexpr int kPExp = 7;        // p * scale is carried times 2^(7 - ve): below 2^15
 
-// Keys of one tile: acc[grp][nt] += codes (tokens grp*16 + {g, g+8}) x R q (columns of tile nt).
+// Keys of one tile: acc[grp][nt] += fields (tokens grp*16 + {g, g+8}) x R q (columns of tile nt).
 template <int D, int B, int NT, int QT>
 __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, int lane, float (&s)[2][NT][4]) {
   constexpr int W = D * B / 128;  // words of a lane's quarter row
@@ -41,10 +47,10 @@ __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, in
     uint32_t a0[4], a1[4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      a0[2 * x] = code_pair<B, W>(w[0], 2 * st + x);
-      a0[2 * x + 1] = code_pair<B, W>(w[1], 2 * st + x);
-      a1[2 * x] = code_pair<B, W>(w[2], 2 * st + x);
-      a1[2 * x + 1] = code_pair<B, W>(w[3], 2 * st + x);
+      a0[2 * x] = field_pair<B, W>(w[0], 2 * st + x);
+      a0[2 * x + 1] = field_pair<B, W>(w[1], 2 * st + x);
+      a1[2 * x] = field_pair<B, W>(w[2], 2 * st + x);
+      a1[2 * x + 1] = field_pair<B, W>(w[3], 2 * st + x);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -57,13 +63,15 @@ __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, in
   }
 }
 
-// Values of one tile: o[mt][nt] += codes^T (features) x (p scale) (tokens), PT terms of the latter.
+// Values of one tile: o[mt][nt] += fields^T (features) x (p scale) (tokens), PT terms of the latter; o[D / 16]
+// the sum of p scale (a row of ones).
 template <int D, int B, int NT, int PT>
 __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&pf)[PT][2][NT][2], int lane,
-                                            float (&o)[D / 16][NT][4]) {
+                                            float (&o)[D / 16 + 1][NT][4]) {
   constexpr int CB = D * B / 64;             // bytes of a lane's eighth row
   constexpr int W = CB >= 4 ? CB / 4 : 1;
   const int g = lane >> 2, m = lane & 3;
+  const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
   for (int grp = 0; grp < 2; ++grp) {
     uint32_t w[4][W];  // tokens 2m, 2m+1, 2m+8, 2m+9
@@ -74,12 +82,12 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
       else load_words<W>(src, w[r]);
     }
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) {
+    for (int mt = 0; mt <= D / 16; ++mt) {
       uint32_t a[4];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        a[f] = code_across<B, W>(w[0], w[1], 2 * mt + f);
-        a[f + 2] = code_across<B, W>(w[2], w[3], 2 * mt + f);
+        a[f] = mt < D / 16 ? field_across<B, W>(w[0], w[1], 2 * mt + f) : ones[f];
+        a[f + 2] = mt < D / 16 ? field_across<B, W>(w[2], w[3], 2 * mt + f) : ones[f];
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -116,8 +124,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   if (rows <= 0) return;
 
   uint2* qf = reinterpret_cast<uint2*>(smem);                        // [QT][NT][NS][32]
-  float* rs = reinterpret_cast<float*>(qf + QT * NT * NS * 32);      // [C] 2^-k of R q's scaling
-  float* qsum = rs + C;                                              // [C]
+  float* qsum = reinterpret_cast<float*>(qf + QT * NT * NS * 32);    // [C]
   float* xm = qsum + C;                                              // [kWarps][C]
   float* xl = xm + kWarps * C;                                       // [kWarps][C]
   float* xz = xl + kWarps * C;                                       // [kWarps][C]
@@ -140,73 +147,99 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   }
   __syncwarp();
 
-  const int pt = min(kTile, 1 << a.p.ps_log2);  // tokens of a piece: a tile spans one or two pages
-  auto fetch = [&](int n) {  // n-th tile of this warp into stage n % stages
-    const int st = n % a.stages;
-    const int piece = lane >> 2, kind = lane & 3;
-    const int tok = (t_first + n * kWarps) * kTile + piece * pt;
-    int page = -1;
-    if (piece * pt < kTile && tok < len) page = page_of(a.p, b, tok, a.err);
-    const uint32_t okm = __ballot_sync(0xffffffffu, page >= 0) & 0x11u;
+  // A tile spans one or two pages (pieces); lane 4 piece + kind copies kind's rows of its piece. The table
+  // entry is read a fetch early.
+  const int ps = 1 << a.p.ps_log2, pt = min(kTile, ps);
+  const int piece = lane >> 2, kind = lane & 3;
+  const bool copies = piece * pt < kTile;
+  const uint32_t rb = kind == 0 ? rbk : kind == 2 ? rbv : 4;
+  const uint32_t from = (kind == 0 ? a.p.kc : kind == 1 ? a.p.ks : kind == 2 ? a.p.vc : a.p.vs) + uint32_t(h) * ps * rb;
+  const uint32_t into = (kind == 0 ? 0 : kind == 1 ? kTile * rbk : kind == 2 ? kTile * (rbk + 4) : kTile * (rbk + 4 + rbv)) +
+                        piece * pt * rb + smem_u32(ring);
+  const int32_t* entries = a.p.table + int64_t(b) * a.p.max_pages;
+  int ahead = t_first * kTile + piece * pt;  // first token of this lane's piece of the tile that is fetched next
+  int id = -1;
+  auto entry = [&] { id = copies && ahead < len ? entries[ahead >> a.p.ps_log2] : -1; };
+  auto fetch = [&](int st) {
+    const bool ok = uint32_t(id) < uint32_t(a.p.n_pages);
+    if (copies && !ok && ahead < len) report_error(a.err, JOLT_ERR_INVALID_ARG);
+    const uint32_t okm = __ballot_sync(0xffffffffu, ok) & 0x11u;
     const uint32_t bar = bar0 + 8 * st;
     if (lane == 0) {
       there[warp * kMaxStages + st] = okm;
       mbar_expect_tx(bar, __popc(okm) * pt * (rbk + rbv + 8));
     }
     __syncwarp();
-    if (page >= 0) {
-      const uint32_t rb = kind == 0 ? rbk : kind == 2 ? rbv : 4;
-      const uint32_t seg = kind == 0 ? a.p.kc : kind == 1 ? a.p.ks : kind == 2 ? a.p.vc : a.p.vs;
-      const uint32_t at = kind == 0 ? 0 : kind == 1 ? kTile * rbk : kind == 2 ? kTile * (rbk + 4) : kTile * (rbk + 4 + rbv);
-      const uint8_t* src = a.p.pool + uint64_t(page) * a.p.page_bytes + seg +
-                           (uint64_t(h) * (1 << a.p.ps_log2) + (tok & ((1 << a.p.ps_log2) - 1))) * rb;
-      bulk_load(smem_u32(ring + st * a.stage_bytes) + at + piece * pt * rb, src, pt * rb, bar);
-    }
+    if (ok)
+      bulk_load(into + st * a.stage_bytes, a.p.pool + uint64_t(uint32_t(id)) * a.p.page_bytes + from + (ahead & (ps - 1)) * rb,
+                pt * rb, bar);
+    ahead += kWarps * kTile;
+    entry();
   };
+  entry();
   for (int n = 0; n < min(a.stages, n_mine); ++n) fetch(n);
 
   // R q of this block's rows as MMA operands: lane (g, m) of k-step st holds column g, the features
-  // that the codes of quarter row m give at that step
+  // that the codes of quarter row m give at that step. One power of two for all rows.
+  float unscale;
   {
     const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
     const float isd = rsqrtf(float(D));
     __half* qh = reinterpret_cast<__half*>(qf);
-    const int nc = 32 / a.p.bk;  // codes of a word
-    for (int r = warp; r < RB; r += kWarps) {
-      float v[E];
+    constexpr int kPer = (RB + kWarps - 1) / kWarps;
+    float v[kPer][E], top = 0.f;
+    float sign[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
+    for (int e = 0; e < E; ++e) sign[e] = rot_sign(a.p.seed, lane * E + e) * a.scale2;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = warp + i * kWarps;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
       if (r < rows) {
-        const int row = r0 + r;
-        const T* x = qb + q_offset(a, row, D) + lane * E;
+        const T* x = qb + q_offset(a, r0 + r, D) + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = ld_as_float(x, e) * a.scale2;
+        for (int e = 0; e < E; ++e) v[i][e] = ld_as_float(x, e) * sign[e];
       }
-      warp_rotate<E>(v, a.p.seed, isd);
-      float top = 0.f, sum = 0.f;
+      if (lane == 0 && r < RB) {  // the elements of H x add up to D x_0
+        qsum[r] = v[i][0] * (float(D) * isd);
+        if (PACK) qsum[r + 4] = qsum[r];
+      }
+      warp_fwht<E>(v[i]);
+      float most = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        top = fmaxf(top, fabsf(v[e]));
-        sum += v[e];
+        v[i][e] *= isd;
+        most = fmaxf(most, fabsf(v[i][e]));
       }
-      top = warp_max(top);
-      sum = warp_sum(sum);
-      // 2^k top in [2^14, 2^15); a zero or non-finite row is left as it is
-      int k = 0;
-      if (top > 0.f && top < INFINITY) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
-      const float up = pow2i(k);
+      if (most < INFINITY) top = fmaxf(top, most);  // a row that is not finite is on its own
+    }
+    top = warp_max(top);
+    if (lane == 0) xm[warp] = top;
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int f = lane * E + e;
-        const int mm = f / (D / 4), fq = f % (D / 4);       // quarter row, feature in it
-        const int w = fq / nc, c = fq % nc;                 // word, code in it
-        const int pair = w * (nc / 2) + c % (nc / 2), hi = c / (nc / 2);
-        const float x = v[e] * up;
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, xm[i]);
+    __syncthreads();
+    int k = 0;  // 2^k top in [2^14, 2^15)
+    if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
+    unscale = pow2i(24 - k);
+    const int lnc = log2_codes(a.p.bk), half = 1 << (lnc - 1);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int f = lane * E + e;
+      const int mm = f / (D / 4), fq = f % (D / 4);       // quarter row, feature in it
+      const int c = fq & (2 * half - 1);                  // code in its word
+      const int pair = ((fq >> lnc) << (lnc - 1)) + (c & (half - 1)), hi = c >> (lnc - 1);
+      const float up = pow2i(k - ((a.p.bk * pair) & 7));  // less the field's place in its byte
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = warp + i * kWarps;
+        if (r >= RB) break;
+        const float x = v[i][e] * up;
         const __half x1 = __float2half_rn(x);
         const __half x2 = __float2half_rn(x - __half2float(x1));
-        const int st = pair >> 1, reg = pair & 1;
         // [term][nt][st][lane = 4 * column + mm][reg][hi]
-        const int at = ((st * 32 + 4 * (r & 7) + mm) * 2 + reg) * 2 + hi;
+        const int at = (((pair >> 1) * 32 + 4 * (r & 7) + mm) * 2 + (pair & 1)) * 2 + hi;
         if (PACK) {
           qh[at] = x1;
           qh[at + 4 * 4 * 4] = x2;  // column r + 4
@@ -216,123 +249,148 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           qh[at + (NT + nt) * NS * 128] = x2;
         }
       }
-      if (lane == 0) {
-        rs[r] = pow2i(-k);
-        qsum[r] = sum;
-        if (PACK) {
-          rs[r + 4] = pow2i(-k);
-          qsum[r + 4] = sum;
-        }
-      }
     }
   }
   __syncthreads();
 
-  float o[NS][NT][4], mx[NT][2], l[NT][2], z[NT][2], crs[NT][2], cqs[NT][2];
+  // A column's (query row's) reference is a whole number, 4 above its maximum when it was last set; it is set
+  // anew only when a thread's four p of a tile add up to more than 2^8, so the usual tile takes no maximum.
+  float o[NS + 1][NT][4], ref[NT][2], l[NT][2], z[NT][2], cqs[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      mx[nt][c] = -INFINITY;
+      ref[nt][c] = -INFINITY;  // before the first every p is too large
       l[nt][c] = z[nt][c] = 0.f;
-      crs[nt][c] = rs[nt * 8 + 2 * m + c];
       cqs[nt][c] = qsum[nt * 8 + 2 * m + c];
     }
 #pragma unroll
-    for (int mt = 0; mt < NS; ++mt)
+    for (int mt = 0; mt <= NS; ++mt)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.f;
   }
-  int ve = -30;  // value scales met so far are below 2^ve
-  const float ok_off = float(1 << (a.p.bk - 1)), ov_off = float(1 << (a.p.bv - 1));
-  for (int n = 0; n < n_mine; ++n) {
-    const int st = n % a.stages;
-    if (!wait_all(bar0 + 8 * st, (n / a.stages) & 1, a.err)) {
+  int ve = -30;            // value scales met so far are below 2^ve
+  float v_lim = pow2i(ve), v_up = pow2i(kPExp - ve);
+  const float ov_off = float(1 << (a.p.bv - 1));
+  for (int n = 0, st = 0, par = 0; n < n_mine; ++n) {
+    if (!wait_all(bar0 + 8 * st, par, a.err)) {
       // gave up (reported): wait, with the same limit, for what is still in flight, then stop
       for (int x = n + 1; x < min(n + a.stages, n_mine); ++x)
         wait_all(bar0 + 8 * (x % a.stages), (x / a.stages) & 1, a.err);
       break;
     }
     const uint8_t* kc = ring + st * a.stage_bytes;
-    const __half2* ksz = reinterpret_cast<const __half2*>(kc + kTile * rbk);
+    const __half2* ksz = reinterpret_cast<const __half2*>(kc + kTile * rbk) + g;
     const uint8_t* vc = kc + kTile * (rbk + 4);
-    const __half2* vsz = reinterpret_cast<const __half2*>(vc + kTile * rbv);
+    const __half2* vsz = reinterpret_cast<const __half2*>(vc + kTile * rbv) + g;
     const uint32_t okm = there[warp * kMaxStages + st];
-    const int tok0 = (t_first + n * kWarps) * kTile;
+    const int left = len - (t_first + n * kWarps) * kTile;  // tokens from this tile's first on
+    const bool whole = left >= kTile && okm == (pt == kTile ? 1u : 0x11u);
 
-    float s[2][NT][4];
+    int unseen = 0;  // bit i: token g + 8 i
+    if (!whole) {
 #pragma unroll
-    for (int grp = 0; grp < 2; ++grp)
+      for (int i = 0; i < 4; ++i)
+        unseen |= int(g + 8 * i >= left || !((pt == kTile ? okm : okm >> (4 * (i >> 1))) & 1)) << i;
+    }
+    // scores to p in place; a tile that calls for new references is done once more, from the keys
+    float s[2][NT][4], sum[NT][2], vsc[4], vze[4];
+    for (bool anew = false;; anew = true) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int grp = 0; grp < 2; ++grp)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[grp][nt][c] = 0.f;
-    if (a.p.bk == 4) keys_tile<D, 4, NT, QT>(kc, qf, lane, s);
-    else if (a.p.bk == 8) keys_tile<D, 8, NT, QT>(kc, qf, lane, s);
-    else keys_tile<D, 2, NT, QT>(kc, qf, lane, s);
-
-    // scale, zero and visibility of this lane's four tokens (rows g + 8 i)
-    float vsc[4], vzr[4];
-    bool seen[4];
-    uint32_t big = 0;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = g + 8 * i;
-      seen[i] = tok0 + t < len && ((pt == kTile ? okm : okm >> (4 * (i >> 1))) & 1);
-      const float2 ks = __half22float2(ksz[t]), vs = __half22float2(vsz[t]);
-      vsc[i] = seen[i] ? vs.x : 0.f;
-      vzr[i] = seen[i] ? vs.y + ov_off * vs.x : 0.f;
-      big = max(big, __float_as_uint(fabsf(vsc[i])));
-      const float kz = ks.y + ok_off * ks.x;
+          for (int c = 0; c < 4; ++c) s[grp][nt][c] = 0.f;
+      if (a.p.bk == 4) keys_tile<D, 4, NT, QT>(kc, qf, lane, s);
+      else if (a.p.bk == 8) keys_tile<D, 8, NT, QT>(kc, qf, lane, s);
+      else keys_tile<D, 2, NT, QT>(kc, qf, lane, s);
+      if (PACK) {  // the two terms of R q
+#pragma unroll
+        for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[grp][0][c] += __shfl_xor_sync(0xffffffffu, s[grp][0][c], 2);
+      }
+      // scales and zeros of this lane's four tokens, rows g + 8 i; scores in log2 units
+      float v_top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 kf = __half22float2(ksz[8 * i]), vf = __half22float2(vsz[8 * i]);
+        const float ks = kf.x * unscale;
+        vsc[i] = vf.x;
+        vze[i] = vf.y + ov_off * vf.x;
+        const bool seen = (unseen >> i & 1) == 0;
+        if (!seen) vsc[i] = vze[i] = 0.f;
+        v_top = fmaxf(v_top, fabsf(vsc[i]));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& x = s[i >> 1][nt][2 * (i & 1) + c];
+            x = x * ks + kf.y * cqs[nt][c];
+            if (!seen) x = -INFINITY;
+          }
+      }
+      if (anew) {
+        const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(v_top));
+        const int ve_new = max(ve, int(big >> 23) - 126);
+        const float drop = pow2i(max(ve - ve_new, -126));
+        ve = ve_new;
+        v_lim = pow2i(min(ve, 127));
+        v_up = pow2i(kPExp - ve);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float t = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            const float now = fmaxf(ref[nt][c], ceilf(t) + kRoom);
+            const float f = now == ref[nt][c] ? 1.f : ex2(ref[nt][c] - now);
+            ref[nt][c] = now;
+            l[nt][c] *= f;
+            z[nt][c] *= f;
+#pragma unroll
+            for (int mt = 0; mt <= NS; ++mt) {
+              o[mt][nt][c] *= f * drop;
+              o[mt][nt][c + 2] *= f * drop;
+            }
+          }
+      }
+      float most = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float& x = s[i >> 1][nt][2 * (i & 1) + c];
-          if (PACK) x += __shfl_xor_sync(0xffffffffu, x, 2);  // the two terms of R q
-          x = seen[i] ? x * crs[nt][c] * ks.x + kz * cqs[nt][c] : -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float& x = s[i >> 1][nt][2 * (i & 1) + c];
+            x = ex2(x - ref[nt][c]);
+            if (unseen >> i & 1) x = 0.f;  // also while ref is -inf
+          }
+          sum[nt][c] = (s[0][nt][c] + s[0][nt][c + 2]) + (s[1][nt][c] + s[1][nt][c + 2]);
+          most = fmaxf(most, sum[nt][c]);
         }
+      if (anew || !__any_sync(0xffffffffu, most > kMost || v_top > v_lim)) break;
     }
-    big = __reduce_max_sync(0xffffffffu, big);
-    const int ve_new = max(ve, int(big >> 23) - 126);
-    const float drop = pow2i(max(ve - ve_new, -126));
-    ve = ve_new;
-    const float up = pow2i(15 - ve);
-
     uint32_t pf[PT][2][NT][2];
-    bool scale_o = drop != 1.f;
-    float al[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float t = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+        l[nt][c] += sum[nt][c];
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-        const float now = fmaxf(mx[nt][c], t);
-        const float ref = now == -INFINITY ? 0.f : now;
-        al[nt][c] = exp2f(mx[nt][c] - ref);
-        scale_o = scale_o || al[nt][c] != 1.f;
-        mx[nt][c] = now;
-        float sum = 0.f, zs = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float& x = s[i >> 1][nt][2 * (i & 1) + c];
-          const float p = exp2f(x - ref);
-          sum += p;
-          zs += p * vzr[i];
-          x = p * (vsc[i] * up);
-        }
-        l[nt][c] = l[nt][c] * al[nt][c] + sum;
-        z[nt][c] = z[nt][c] * al[nt][c] + zs;
+        for (int i = 0; i < 4; ++i) z[nt][c] += s[i >> 1][nt][2 * (i & 1) + c] * vze[i];
       }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vsc[i] *= v_up;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float x0 = s[grp][nt][2 * i], x1 = s[grp][nt][2 * i + 1];
+          const float x0 = s[grp][nt][2 * i] * vsc[2 * grp + i], x1 = s[grp][nt][2 * i + 1] * vsc[2 * grp + i];
           uint32_t hi = h2_pack(x0, x1);
           if (sizeof(T) == 4) {
             const float2 f = h2_floats(hi);
@@ -344,25 +402,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           }
           pf[0][grp][nt][i] = trans8x8(hi);
         }
-    if (__any_sync(0xffffffffu, scale_o)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float f = al[nt][c] * drop;
-#pragma unroll
-          for (int mt = 0; mt < NS; ++mt) {
-            o[mt][nt][c] *= f;
-            o[mt][nt][c + 2] *= f;
-          }
-        }
-    }
     if (a.p.bv == 4) values_tile<D, 4, NT, PT>(vc, pf, lane, o);
     else if (a.p.bv == 8) values_tile<D, 8, NT, PT>(vc, pf, lane, o);
     else values_tile<D, 2, NT, PT>(vc, pf, lane, o);
     __syncwarp();  // every lane is done with the stage
-    if (n + a.stages < n_mine) fetch(n + a.stages);
+    if (n + a.stages < n_mine) fetch(st);
+    if (++st == a.stages) {
+      st = 0;
+      par ^= 1;
+    }
   }
+
   // ---- the warps' partial results into one ----
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -373,10 +423,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
         z[nt][c] += __shfl_xor_sync(0xffffffffu, z[nt][c], x);
       }
-      if (g == 0) xm[warp * C + nt * 8 + 2 * m + c] = mx[nt][c];
+      if (g == 0) xm[warp * C + nt * 8 + 2 * m + c] = ref[nt][c];
     }
   __syncthreads();
-  const float unit = pow2i(ve - 15);
+  // fields' powers of two, and o sum(p scale), out of the outputs
+  const float unit = pow2i(ve - kPExp);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -385,16 +436,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, xm[w * C + col]);
-      const float f = mx[nt][c] == -INFINITY ? 0.f : exp2f(mx[nt][c] - top);
+      const float f = ref[nt][c] == -INFINITY ? 0.f : ex2(ref[nt][c] - top);
       if (g == 0) {
         xl[warp * C + col] = l[nt][c] * f;
         xz[warp * C + col] = z[nt][c] * f;
       }
-      mx[nt][c] = top;
+      ref[nt][c] = top;
+      const float off = ov_off * o[NS][nt][c];
 #pragma unroll
       for (int mt = 0; mt < NS; ++mt) {
-        o[mt][nt][c] *= f * unit;
-        o[mt][nt][c + 2] *= f * unit;
+        o[mt][nt][c] = (o[mt][nt][c] * pow2i(24 - ((2 * mt * a.p.bv) & 7)) - off) * (f * unit);
+        o[mt][nt][c + 2] = (o[mt][nt][c + 2] * pow2i(24 - (((2 * mt + 1) * a.p.bv) & 7)) - off) * (f * unit);
         if (PACK) {
           o[mt][nt][c] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c], 2);
           o[mt][nt][c + 2] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c + 2], 2);
@@ -431,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
       }
       const int row = r0 + col;
       const int64_t part = out_row(a, b, h, row) * a.parts + split;
-      if (g == 0) a.ml[part] = make_float2(mx[nt][c], ls);
-      if (mx[nt][c] == -INFINITY) continue;
+      if (g == 0) a.ml[part] = make_float2(ref[nt][c], ls);
+      if (ref[nt][c] == -INFINITY) continue;
       float* dst = a.acc + part * D + g * (D / 8);
 #pragma unroll
       for (int mt = 0; mt < NS; mt += 2)
@@ -543,7 +595,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const int budget = (t.nt == 1 ? 100 : 190) * 1024;
   t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
   const int C = 8 * t.nt, qt = t.pack ? 1 : 2;
-  const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 8 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
+  const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 4 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
   const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
   const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
   const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);

@@ -78,6 +78,11 @@ __device__ __forceinline__ Work work_of(const TreeArgs& a) {
   w.split = split;
   return w;
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 __device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
   uint32_t y;

@@ -92,12 +92,6 @@ __device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 16 lanes x 32 columns of tensor memory: register 4a + {0, 1} = (lane g, columns 8a + 2m, +1), + {2, 3} the
 // same of lane g + 8.
 __device__ __forceinline__ void ld_16x256(uint32_t t, uint32_t (&r)[16]) {
@@ -140,13 +134,6 @@ __device__ __forceinline__ void ld_wait(uint32_t (&x)[16]) {
 //
 // Keys: codes are whole numbers c 2^-24 already as the f16 bits of their fields (f16's subnormals, with a
 // field's place in its byte a further power of two that R q is divided by): one mask a pair.
-template <int B, int W>
-__device__ __forceinline__ uint32_t field_pair(const uint32_t (&w)[W], int i) {
-  constexpr int H = 16 / B, F = 8 / B;  // pairs a word, fields a byte
-  const int p = i % H;
-  const uint32_t x = p >= F ? w[i / H] >> 8 : w[i / H];
-  return x & (0x00010001u * (((1u << B) - 1) << (B * (p % F))));
-}
 template <int D, int B>
 __device__ __forceinline__ void widen_keys(const uint32_t (&w)[4][D * B / 128], uint8_t* tile, const int (&off)[D / 32]) {
 #pragma unroll
