@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, m = lane & 3;
-  const Work wk = work_of(a);
+  Work wk;
+  if (!work_of<kTile>(a, &wk)) return;
   const int h = wk.h, r0 = wk.block * RB, b = wk.b, split = wk.split;
   if (split == a.splits) {
     draft_part<T, D, RB, kThreads>(a, b, h, r0, smem);
@@ -132,11 +133,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   uint32_t* there = reinterpret_cast<uint32_t*>(bars + kWarps * kMaxStages);  // pieces of a stage that hold tokens
   uint8_t* ring0 = reinterpret_cast<uint8_t*>(there + kWarps * kMaxStages);
 
-  const int len = pages_len(a.p, b, a.err);
-  const int tiles = (len + kTile - 1) / kTile;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int t_end = min(tiles, (split + 1) * per);
-  const int t_first = split * per + warp;
+  const int len = wk.len, t_first = wk.tile0 + warp, t_end = wk.tile0 + wk.n_tiles;
   const int n_mine = t_first < t_end ? (t_end - t_first + kWarps - 1) / kWarps : 0;
   const int rbk = D * a.p.bk / 8, rbv = D * a.p.bv / 8;
   uint8_t* ring = ring0 + warp * a.stages * a.stage_bytes;
@@ -319,8 +316,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         const float ks = kf.x * unscale;
         vsc[i] = vf.x;
         vze[i] = vf.y + ov_off * vf.x;
-        const bool seen = (unseen >> i & 1) == 0;
-        if (!seen) vsc[i] = vze[i] = 0.f;
+        if (!whole && (unseen >> i & 1)) vsc[i] = vze[i] = 0.f;
         v_top = fmaxf(v_top, fabsf(vsc[i]));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -328,7 +324,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           for (int c = 0; c < 2; ++c) {
             float& x = s[i >> 1][nt][2 * (i & 1) + c];
             x = x * ks + kf.y * cqs[nt][c];
-            if (!seen) x = -INFINITY;
           }
       }
       if (anew) {
@@ -342,7 +337,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float t = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+            float t = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(unseen >> i & 1)) t = fmaxf(t, s[i >> 1][nt][2 * (i & 1) + c]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
             const float now = fmaxf(ref[nt][c], ceilf(t) + kRoom);
@@ -366,8 +364,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           for (int i = 0; i < 4; ++i) {
             float& x = s[i >> 1][nt][2 * (i & 1) + c];
             x = ex2(x - ref[nt][c]);
-            if (unseen >> i & 1) x = 0.f;  // also while ref is -inf
           }
+        }
+      if (!whole) {  // also while ref is -inf
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (unseen >> i & 1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[i >> 1][nt][2 * (i & 1)] = s[i >> 1][nt][2 * (i & 1) + 1] = 0.f;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
           sum[nt][c] = (s[0][nt][c] + s[0][nt][c + 2]) + (s[1][nt][c] + s[1][nt][c + 2]);
           most = fmaxf(most, sum[nt][c]);
         }
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
 // One warp a row: joins the splits, rotates their sum back, then adds the drafted tokens' part and the
 // prefix. Launched while k_tree still runs (its grid starts as k_tree's blocks leave); it waits for
 // k_tree's end before it reads anything.
-template <typename T, int D>
+template <typename T, int D, int TILE>
 __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -509,11 +519,13 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
   const int64_t bi = row / a.n_q;
   const int b = int(bi / a.n_new), i = int(bi % a.n_new);
   if (i >= draft_count(a, b)) return;
+  const int splits = splits_of<TILE>(a, b, lane);
   float2 p[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int s = lane + 32 * x;
-    p[x] = s < a.parts ? a.ml[row * a.parts + s] : make_float2(-INFINITY, 0.f);
+    const bool there = s < splits || (draft && s == a.splits);
+    p[x] = there ? a.ml[row * a.parts + s] : make_float2(-INFINITY, 0.f);
   }
   const float pre = a.prefix_lse ? a.prefix_lse[row] * 1.4426950408889634f : -INFINITY;
   const float top = fmaxf(warp_max(fmaxf(p[0].x, p[1].x)), pre);
@@ -527,12 +539,30 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   const float* acc = a.acc + row * a.parts * D + lane * E;
-  for (int s = 0; s < a.splits; ++s) {
-    const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
-    if (f != 0.f) {
+  constexpr int kBatch = 8;  // splits whose loads are in flight together
+  for (int s0 = 0; s0 < splits; s0 += kBatch) {
+    float f[kBatch], x[kBatch][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(s) * D + e];
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i;
+      f[i] = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
+      if (s >= splits) f[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      if (f[i] != 0.f) {  // a split that saw nothing has left nothing
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(acc + int64_t(s) * D);
+          x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(acc + int64_t(s) * D);
+          x[i][0] = y.x, x[i][1] = y.y;
+        }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f[i] * x[i][e];
   }
   if (a.perm) {
     __shared__ float row_s[4][D];
@@ -568,8 +598,8 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 // ---- host -------------------------------------------------------------------------------------------
 
 struct TreePlan {
-  int nt, blocks, splits, parts, stages, stage_bytes;
-  bool pack, tc;
+  int nt, blocks, splits, shares, least, parts, stages, stage_bytes;
+  bool pack, tc, balanced;
   size_t smem, ws_acc, ws_total;
 };
 
@@ -579,18 +609,13 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   if (rows > 32 && p.io_dtype == JOLT_BF16) {
     t.tc = true;
     t.blocks = (rows + 127) / 128;
-    const int64_t units = int64_t(batch) * p.n_kv * t.blocks;
-    const int64_t tiles = (int64_t(max_pages) * p.page_size + 127) / 128;
-    t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + 1) / 2, 148 / units})));
+    t.least = 2;
     t.smem = tree_tc_smem(p.d_h);
   } else {
   t.pack = rows <= 4;
   t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   t.blocks = (rows + 8 * t.nt - 1) / (8 * t.nt);
-  const int64_t units = int64_t(batch) * p.n_kv * t.blocks;
-  const int64_t tiles = (int64_t(max_pages) * p.page_size + kTile - 1) / kTile;
-  const int resident = 148 * (t.nt == 1 ? 2 : 1);
-  t.splits = int(std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (tiles + kWarps - 1) / kWarps, resident / units})));
+  t.least = kWarps;
   t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
   const int budget = (t.nt == 1 ? 100 : 190) * 1024;
   t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
@@ -601,6 +626,14 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
   t.smem = std::max(head + std::max(ring, red), draft);
   }
+  // one block an SM for each 128 rows, or two where the registers allow: as many shares as are resident at once
+  const int heads = p.n_kv * t.blocks, resident = 148 * (!t.tc && t.nt == 1 ? 2 : 1);
+  const int64_t tile = t.tc ? 128 : kTile;
+  const int64_t tiles = (int64_t(max_pages) * p.page_size + tile - 1) / tile;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, (tiles + t.least - 1) / t.least));
+  t.balanced = batch <= kMaxBalanced && resident / heads >= batch;
+  t.shares = t.balanced ? int(std::min<int64_t>(resident / heads, most * batch)) : batch;
+  t.splits = t.balanced ? int(std::min<int64_t>(most, t.shares)) : 1;
   t.parts = t.splits + 1;
   const size_t nrows = size_t(batch) * n_new * n_q;
   t.ws_acc = align_up(sizeof(WsHeader) + nrows * t.parts * sizeof(float2), 256);
@@ -613,7 +646,7 @@ bool tree_dims_ok(const jolt_pages* p, int batch, int n_new, int n_q, int max_pa
          n_q % p->n_kv == 0 && n_q <= 65536 && max_pages >= 1 && int64_t(max_pages) * p->page_size <= (int64_t(1) << 24);
 }
 
-template <typename T, int D>
+template <typename T, int D, int TILE>
 jolt_status launch_merge(const TreeArgs& a, bool draft, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned((int64_t(a.batch) * a.n_new * a.n_q + 3) / 4));
@@ -624,24 +657,24 @@ jolt_status launch_merge(const TreeArgs& a, bool draft, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  JOLT_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tree_merge<T, D>, a, draft));
+  JOLT_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_tree_merge<T, D, TILE>, a, draft));
   return JOLT_OK;
 }
 
 template <typename T, int D, int NT, bool PACK>
 jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
   JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree<T, D, NT, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(t.smem)));
-  const unsigned grid = unsigned(t.splits + (draft ? 1 : 0)) * a.p.n_kv * t.blocks * a.batch;
+  const unsigned grid = unsigned(t.shares + (draft ? a.batch : 0)) * a.p.n_kv * t.blocks;
   k_tree<T, D, NT, PACK><<<grid, kThreads, t.smem, st>>>(a);
   JOLT_CUDA_TRY(cudaGetLastError());
-  return launch_merge<T, D>(a, draft, st);
+  return launch_merge<T, D, kTile>(a, draft, st);
 }
 
 template <typename T, int D>
 jolt_status launch_tree_d(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
   if (t.tc) {
     const jolt_status r = launch_tree_tc(a, D, draft, t.smem, st);
-    return r != JOLT_OK ? r : launch_merge<T, D>(a, draft, st);
+    return r != JOLT_OK ? r : launch_merge<T, D, 128>(a, draft, st);
   }
   if (t.pack) return launch_tree<T, D, 1, true>(a, t, draft, st);
   if (t.nt == 1) return launch_tree<T, D, 1, false>(a, t, draft, st);
@@ -680,7 +713,7 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   if (!rows_ok(q, q_stride_b, q_stride_t) || (!k != !v) || (!prefix_out != !prefix_lse)) return JOLT_ERR_INVALID_ARG;
   if (k && (!rows_ok(k, kv_stride_b, kv_stride_t) || !rows_ok(v, kv_stride_b, kv_stride_t))) return JOLT_ERR_INVALID_ARG;
   const TreePlan t = tree_plan(*pages, batch, n_new, n_q, max_pages);
-  if (int64_t(batch) * pages->n_kv * t.blocks * (t.splits + 1) > (1 << 30)) return JOLT_ERR_INVALID_ARG;
+  if (int64_t(batch + t.shares) * pages->n_kv * t.blocks > (1 << 30)) return JOLT_ERR_INVALID_ARG;
   if (ws_bytes < t.ws_total) return JOLT_ERR_WORKSPACE;
   uint8_t* w = static_cast<uint8_t*>(ws);
   TreeArgs a{};
@@ -708,6 +741,9 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   a.gq_magic = uint32_t(((uint64_t(1) << 32) + a.gq - 1) / a.gq);
   a.perm = t.tc ? pages->b_v : 0;
   a.splits = t.splits;
+  a.shares = t.shares;
+  a.least = t.least;
+  a.balanced = t.balanced;
   a.parts = k ? t.parts : t.splits;
   a.batch = batch;
   a.blocks = t.blocks;

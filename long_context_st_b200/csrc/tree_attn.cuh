@@ -26,7 +26,11 @@ struct TreeArgs {
   float* acc;   // [rows][parts][D]
   int32_t* err;
   float scale2;  // attn_scale * log2(e): scores are kept in log2 units
-  int n_new, n_q, gq, splits, parts, batch, blocks, stages, stage_bytes;
+  int n_new, n_q, gq, parts, batch, blocks, stages, stage_bytes;
+  int splits;        // most splits of a sequence; the drafted tokens' part follows them
+  int shares;        // blocks a (KV head, row block) has for all sequences' splits
+  int least;         // tiles of a split at least
+  int balanced;      // splits of equal size over all sequences (else `splits` of every sequence)
   uint32_t gq_magic;  // ceil(2^32 / gq)
   int perm;           // features of acc are in tree_tc.cu's order for this many value bits (0: their own order)
 };
@@ -56,27 +60,107 @@ __device__ __forceinline__ int64_t out_row(const TreeArgs& a, int b, int h, int 
   const int t = row_token(a, row);
   return (int64_t(b) * a.n_new + t) * a.n_q + h * a.gq + (row - t * a.gq);
 }
-// What a block works on: the pages' splits of all (sequence, KV head, row block) first, then the drafted
-// tokens' parts (split == splits), which are short and fill the SMs that the splits leave.
-struct Work {
-  int b, h, block, split;
+// ---- how the pages' tokens are divided ----
+// A (KV head, row block) has `shares` blocks for the tiles of all sequences. Balanced: a split has c tiles, the
+// least c (of a few) for which all sequences' splits number at most `shares`, so a ragged batch keeps every
+// block equally long (lengths 64K, 56K, 48K, 40K: 23% over a division of each sequence by the same number).
+// The lengths are on the device, so every warp works this out for itself; lane i has sequences 4 i .. + 3.
+constexpr int kMaxBalanced = 128;  // sequences
+struct Shares {
+  int tiles[4], c;
 };
-__device__ __forceinline__ Work work_of(const TreeArgs& a) {
-  const int units = a.batch * a.p.n_kv * a.blocks;
-  int id = blockIdx.x, split = a.splits;
-  if (id < units * a.splits) {
-    split = id % a.splits;
-    id /= a.splits;
-  } else {
-    id -= units * a.splits;
+template <int TILE>
+__device__ __forceinline__ Shares shares_of(const TreeArgs& a, int lane) {
+  Shares s;
+  const int cap = a.p.max_pages << a.p.ps_log2;
+  int sum = 0, top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = lane * 4 + i;
+    const int raw = b < a.batch ? a.p.lens[b] : 0, len = min(max(raw, 0), cap);
+    if (len != raw) report_error(a.err, JOLT_ERR_INVALID_ARG);
+    s.tiles[i] = (len + TILE - 1) / TILE;
+    sum += s.tiles[i];
+    top = max(top, s.tiles[i]);
   }
-  Work w;
-  w.block = id % a.blocks;
-  id /= a.blocks;
-  w.h = id % a.p.n_kv;
-  w.b = id / a.p.n_kv;
-  w.split = split;
-  return w;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int least = max(a.least, (top + a.splits - 1) / a.splits);
+  // c = sum / (shares - k) does for some k <= batch: each sequence rounds up by less than one
+  const int step = max(1, a.batch >> 3);
+  for (int k = 0;; k += step) {
+    const int left = max(a.shares - min(k, a.batch), 1);
+    s.c = max(least, (sum + left - 1) / left);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += (s.tiles[i] + s.c - 1) / s.c;
+    if (k >= a.batch || int(__reduce_add_sync(0xffffffffu, n)) <= a.shares) return s;
+  }
+}
+// What a block works on: a split's tiles, or the drafted tokens (split == splits; these blocks come last:
+// they are short and fill the SMs that the splits leave).
+struct Work {
+  int b, h, block, split, tile0, n_tiles, len;
+};
+template <int TILE>
+__device__ __forceinline__ bool work_of(const TreeArgs& a, Work* w) {
+  const int heads = a.p.n_kv * a.blocks, lane = threadIdx.x & 31;
+  int id = int(blockIdx.x) / heads;
+  const int hb = int(blockIdx.x) - id * heads;
+  w->h = hb / a.blocks;
+  w->block = hb - w->h * a.blocks;
+  w->tile0 = w->n_tiles = w->len = 0;
+  if (id >= a.shares) {
+    w->b = id - a.shares;
+    w->split = a.splits;
+    return true;
+  }
+  int c, tiles;
+  if (a.balanced) {
+    const Shares s = shares_of<TILE>(a, lane);
+    int n[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine += n[i] = (s.tiles[i] + s.c - 1) / s.c;
+    int first = mine;  // splits before this lane's sequences
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, first, x);
+      if (lane >= x) first += y;
+    }
+    first -= mine;
+    int found = -1, split = 0, t = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (id >= first && id < first + n[i]) found = lane * 4 + i, split = id - first, t = s.tiles[i];
+      first += n[i];
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, found >= 0);
+    if (!who) return false;  // more blocks than splits
+    const int src = __ffs(who) - 1;
+    w->b = __shfl_sync(0xffffffffu, found, src);
+    w->split = __shfl_sync(0xffffffffu, split, src);
+    tiles = __shfl_sync(0xffffffffu, t, src);
+    c = s.c;
+    w->len = pages_len(a.p, w->b, a.err);
+  } else {
+    w->b = id / a.splits;
+    w->split = id - w->b * a.splits;
+    w->len = pages_len(a.p, w->b, a.err);
+    tiles = (w->len + TILE - 1) / TILE;
+    c = (tiles + a.splits - 1) / a.splits;
+  }
+  w->tile0 = w->split * c;
+  w->n_tiles = max(0, min(tiles, w->tile0 + c) - w->tile0);
+  return true;
+}
+// Splits of sequence b (of which a partial result is there).
+template <int TILE>
+__device__ __forceinline__ int splits_of(const TreeArgs& a, int b, int lane) {
+  if (!a.balanced) return a.splits;
+  const Shares s = shares_of<TILE>(a, lane);
+  const int i = b & 3;
+  const int t = __shfl_sync(0xffffffffu, i == 0 ? s.tiles[0] : i == 1 ? s.tiles[1] : i == 2 ? s.tiles[2] : s.tiles[3], b >> 2);
+  return (t + s.c - 1) / s.c;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -644,14 +644,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
   extern __shared__ uint8_t raw[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Work wk = work_of(a);
+  Work wk;
+  if (!work_of<kTok>(a, &wk)) return;
   const int h = wk.h, r0 = wk.block * kRows, b = wk.b, split = wk.split;
   uint8_t* smem = align_smem_1024(raw);
   if (split == a.splits) {
     draft_part<__nv_bfloat16, D, kRows, kThreads>(a, b, h, r0, smem);
     return;
   }
-  const int len = pages_len(a.p, b, a.err);  // read with the count, not after it
   const int rows = min(kRows, draft_count(a, b) * a.gq - r0);
   if (rows <= 0) return;
   Ctx<D> c;
@@ -660,10 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
   c.bar0 = c.sb + S::bars;
   c.h = h;
   c.b = b;
-  c.len = len;
-  const int tiles = (c.len + kTok - 1) / kTok, per = (tiles + a.splits - 1) / a.splits;
-  c.tile0 = split * per;
-  c.n_tiles = max(0, min(tiles, c.tile0 + per) - c.tile0);
+  c.len = wk.len;
+  c.tile0 = wk.tile0;
+  c.n_tiles = wk.n_tiles;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::slot);
   if (warp == 24) {
     tmem_alloc(smem_u32(slot), 512);
@@ -780,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
 template <int D>
 jolt_status launch(const TreeArgs& a, bool draft, size_t smem, cudaStream_t st) {
   JOLT_CUDA_TRY(cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-  const unsigned grid = unsigned(a.splits + (draft ? 1 : 0)) * a.p.n_kv * a.blocks * a.batch;
+  const unsigned grid = unsigned(a.shares + (draft ? a.batch : 0)) * a.p.n_kv * a.blocks;
   k_tree_tc<D><<<grid, kThreads, smem, st>>>(a);
   JOLT_CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
