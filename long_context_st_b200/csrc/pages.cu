@@ -110,7 +110,7 @@ __device__ __forceinline__ void store_codes(const uint32_t (&c)[8 * J], uint8_t*
 // the product lies within levels * 2^-20 of a half-integer; only then is the division done. The
 // product is first clipped to (-1/2, levels + 1/2), where clipping and rounding commute.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_append(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
   constexpr int J = D / 32, N = 8 * J;  // pieces and elements of a lane
   const int lane = threadIdx.x & 31, g = lane >> 2, m = lane & 3;
   const int kv = blockIdx.y;
@@ -297,12 +297,9 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
 // step's) by butterflies of the accumulators. One rounding for scale / sqrt(D), one product, one
 // rounding to the output's type.
 template <typename T, int D, int B>
-__device__ __forceinline__ void read_tile(const uint8_t* codes, const __half2* szs, int g, int m, float isd, uint32_t neg,
-                                          T* out, int64_t first, int lo, int hi) {
+__device__ __forceinline__ void read_tile(const uint32_t (&w)[2][D * B / 128], const __half2 (&szs)[2], int g, int m, float isd,
+                                          uint32_t neg, T* out, int64_t first, int lo, int hi) {
   constexpr int J = D / 32, NS = D / 16, W = J * B / 4;
-  uint32_t w[2][W];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) load_codes<B, J>(codes + (g + 8 * r) * (D * B / 8), m, w[r]);
   // sign matrix: rows k = (lane m, register x, half hi), columns n = nt*8 + (m' * 2 + c): the output
   // bit of m is m', that of x is c, that of hi is nt
   const int mm = (g >> 1) & 3, c = g & 1;
@@ -345,7 +342,7 @@ __device__ __forceinline__ void read_tile(const uint8_t* codes, const __half2* s
   for (int r = 0; r < 2; ++r) {
     const int t = g + 8 * r;
     if (t < lo || t >= hi) continue;
-    const float2 sz = __half22float2(szs[t]);
+    const float2 sz = __half22float2(szs[r]);
     const float f = sz.x * isd;
     const f2 ff = f2_make(f, f);
     const float z0 = m == 0 ? (sz.y + float(1 << (B - 1)) * sz.x) * (isd * float(D)) : 0.f;
@@ -368,8 +365,59 @@ __device__ __forceinline__ void read_tile(const uint8_t* codes, const __half2* s
   }
 }
 
+// The tiles of a warp, each one's codes loaded while the one before is worked on, and its table entry
+// before that. A tile without a page (reported) is read from page 0 and not written.
+template <typename T, int D, int B>
+__device__ __forceinline__ void read_tiles(const ReadArgs& a, int kv, int h, int b, int g, int m, int from, int end, T* out,
+                                           uint32_t neg) {
+  constexpr int W = D * B / 128;
+  const float isd = rsqrtf(float(D));
+  const int ps = 1 << a.p.ps_log2;
+  const int32_t* entries = a.p.table + int64_t(b) * a.p.max_pages;
+  const int step = gridDim.x * kWarps, last = (end - 1) >> 4;
+  int t = (from >> 4) + blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t > last) return;
+  uint32_t w[2][W];
+  __half2 sz[2];
+  auto load = [&](int tile, int id) {
+    const bool ok = uint32_t(id) < uint32_t(a.p.n_pages);
+    if (!ok) report_error(a.err, JOLT_ERR_INVALID_ARG);
+    const uint8_t* base = a.p.pool + (ok ? uint64_t(uint32_t(id)) * a.p.page_bytes : 0);
+    const uint32_t row = uint32_t(h) * ps + ((tile * 16) & (ps - 1)) + g;
+    const uint8_t* codes = base + (kv ? a.p.vc : a.p.kc) + uint64_t(row) * (D * B / 8);
+    const __half2* s = reinterpret_cast<const __half2*>(base + (kv ? a.p.vs : a.p.ks)) + row;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      load_codes<B, D / 32>(codes + 8 * r * (D * B / 8), m, w[r]);
+      sz[r] = s[8 * r];
+    }
+    return ok;
+  };
+  bool ok = load(t, entries[(t * 16) >> a.p.ps_log2]);
+  int id = t + step <= last ? entries[((t + step) * 16) >> a.p.ps_log2] : 0;
+  while (true) {
+    uint32_t now[2][W];
+    __half2 now_sz[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) now[r][i] = w[r][i];
+      now_sz[r] = sz[r];
+    }
+    const bool now_ok = ok;
+    const int next = t + step;
+    if (next <= last) {
+      ok = load(next, id);
+      if (next + step <= last) id = entries[((next + step) * 16) >> a.p.ps_log2];
+    }
+    if (now_ok) read_tile<T, D, B>(now, now_sz, g, m, isd, neg, out, int64_t(t) * 16 - from, from - t * 16, end - t * 16);
+    if (next > last) return;
+    t = next;
+  }
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) k_read(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_read(const ReadArgs a) {
   const int lane = threadIdx.x & 31, g = lane >> 2, m = lane & 3;
   const int kv = blockIdx.y >= a.p.n_kv, h = blockIdx.y - kv * a.p.n_kv, b = blockIdx.z;
   T* out = static_cast<T*>(a.out[kv]);
@@ -380,25 +428,14 @@ __global__ void __launch_bounds__(kThreads) k_read(const ReadArgs a) {
     return;
   }
   const int len = pages_len(a.p, b, a.err);
-  const int end = min(len, from > len ? len : from + min(a.n_out, len - from));
-  if (from >= end) return;
+  if (from >= len) return;
+  const int end = from + min(a.n_out, len - from);
   out += int64_t(b) * a.stride_b + int64_t(h) * a.stride_h;
   const uint32_t neg = lane_signs<D>(a.p.seed, lane);
-  const float isd = rsqrtf(float(D));
   const int bits = kv ? a.p.bv : a.p.bk;
-  for (int t = (from >> 4) + blockIdx.x * kWarps + (threadIdx.x >> 5); t * 16 < end; t += gridDim.x * kWarps) {
-    const int page = page_of(a.p, b, t * 16, a.err);
-    if (page < 0) continue;
-    const uint8_t* base = a.p.pool + uint64_t(page) * a.p.page_bytes;
-    const int row = (h << a.p.ps_log2) + ((t * 16) & ((1 << a.p.ps_log2) - 1));
-    const uint8_t* codes = base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
-    const __half2* szs = reinterpret_cast<const __half2*>(base + (kv ? a.p.vs : a.p.ks)) + row;
-    const int64_t first = int64_t(t) * 16 - from;
-    const int lo = from - t * 16, hi = end - t * 16;  // rows of the tile that are wanted
-    if (bits == 4) read_tile<T, D, 4>(codes, szs, g, m, isd, neg, out, first, lo, hi);
-    else if (bits == 8) read_tile<T, D, 8>(codes, szs, g, m, isd, neg, out, first, lo, hi);
-    else read_tile<T, D, 2>(codes, szs, g, m, isd, neg, out, first, lo, hi);
-  }
+  if (bits == 4) read_tiles<T, D, 4>(a, kv, h, b, g, m, from, end, out, neg);
+  else if (bits == 8) read_tiles<T, D, 8>(a, kv, h, b, g, m, from, end, out, neg);
+  else read_tiles<T, D, 2>(a, kv, h, b, g, m, from, end, out, neg);
 }
 
 // Checks shared by the calls over a pool.

@@ -19,6 +19,8 @@ struct RopeArgs {
   int64_t n_tokens;
   float scaling;
   int d, rot, tb, inverse;
+  int rows_at;      // k_rope_vec: rows a thread takes (of kRows)
+  uint32_t magic;   // ceil(2^32 / heads)
 };
 
 constexpr int kThreads = 256;
@@ -73,76 +75,79 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::N]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One pass over q and k: a block takes tb tokens, forms their table once for all heads, and each
-// thread turns 16-byte pieces of one place in the head, kRows rows (token, head) at a time with all
-// their loads in flight: half layout, a piece of each half; interleaved, one piece of whole pairs.
-// Pieces past rot_dim are copied. x and y may be the same memory: every piece is read and written by
-// one thread.
+// One pass over q and k, whose heads are taken as one run of (token, head) rows: a thread turns the 16-byte
+// pieces of one place in the head for up to kRows rows, with all their loads in flight; half layout, a
+// piece of each half; interleaved, one piece of whole pairs. Pieces past rot_dim are copied. The block's
+// tokens' table is formed once for all their heads. x and y may be the same memory: every piece is read and
+// written by one thread.
 constexpr int kRows = 4;
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
   constexpr int V = Vec<T>::N;
   extern __shared__ float2 cs[];
-  const int64_t t0 = int64_t(blockIdx.x) * a.tb;
-  const int nt = int(a.n_tokens - t0 < a.tb ? a.n_tokens - t0 : a.tb);
-  rope_table(a, t0, nt, cs);
   const int half = a.rot >> 1;
   const int rot_units = HALF ? half / V : a.rot / V;
   const int units = rot_units + (a.d - a.rot) / V;  // pieces of a head, at most 128
-  const int heads = a.t[0].heads + a.t[1].heads;
-  const int u = threadIdx.x % units, at_once = kThreads / units;
-  if (int(threadIdx.x) >= at_once * units) return;
+  const uint32_t heads = a.t[0].heads + a.t[1].heads;
+  const int at_once = kThreads / units, rr = threadIdx.x / units, u = threadIdx.x - rr * units;
+  const uint64_t first = uint64_t(blockIdx.x) * (at_once * a.rows_at), total = uint64_t(a.n_tokens) * heads;
+  const int rows = int(total - first < uint64_t(at_once * a.rows_at) ? total - first : at_once * a.rows_at);
+  const int64_t t0 = first / heads;
+  const uint32_t h0 = uint32_t(first - t0 * heads);
+  // token of the block's x-th row, counted from t0's first head: at most 1024 rows, so one of two tokens
+  // where there are more heads
+  auto token = [&](uint32_t x) -> int { return heads == 1 ? x : heads > 1024 ? x >= heads : __umulhi(x, a.magic); };
   const bool turn = u < rot_units;
   const int at = turn ? u * V : a.rot + (u - rot_units) * V;
-  const int rows = nt * heads;
-  for (int r0 = threadIdx.x / units; r0 < rows; r0 += kRows * at_once) {
-    uint4 pa[kRows], pb[kRows];
-    T* dst[kRows];
-    int tok[kRows];
+  uint4 pa[kRows], pb[kRows];
+  T* dst[kRows];
+  int tok[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = r0 + i * at_once;
-      if (row >= rows) break;
-      tok[i] = row / heads;
-      int h = row - tok[i] * heads;
-      const int which = h >= a.t[0].heads;
-      const RopeTensor& x = a.t[which];
-      if (which) h -= a.t[0].heads;
-      const T* src = static_cast<const T*>(x.x) + (t0 + tok[i]) * x.sx + int64_t(h) * a.d + at;
-      dst[i] = static_cast<T*>(x.y) + (t0 + tok[i]) * x.sy + int64_t(h) * a.d + at;
-      pa[i] = *reinterpret_cast<const uint4*>(src);
-      if (HALF && turn) pb[i] = *reinterpret_cast<const uint4*>(src + half);
+  for (int i = 0; i < kRows; ++i) {
+    const int row = rr + i * at_once;
+    tok[i] = -1;
+    if (i >= a.rows_at || row >= rows || rr >= at_once) continue;
+    const uint32_t x = h0 + row;
+    tok[i] = token(x);
+    uint32_t h = x - tok[i] * heads;
+    const int which = h >= uint32_t(a.t[0].heads);
+    const RopeTensor& y = a.t[which];
+    if (which) h -= a.t[0].heads;
+    const T* src = static_cast<const T*>(y.x) + (t0 + tok[i]) * y.sx + int64_t(h) * a.d + at;
+    dst[i] = static_cast<T*>(y.y) + (t0 + tok[i]) * y.sy + int64_t(h) * a.d + at;
+    pa[i] = *reinterpret_cast<const uint4*>(src);
+    if (HALF && turn) pb[i] = *reinterpret_cast<const uint4*>(src + half);
+  }
+  rope_table(a, t0, token(h0 + rows - 1) + 1, cs);  // under the loads
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (tok[i] < 0) continue;
+    if (!turn) {
+      *reinterpret_cast<uint4*>(dst[i]) = pa[i];
+      continue;
     }
+    const float2* c = cs + tok[i] * half;
+    float p[V], y[V];
+    unpack<T>(pa[i], p);
+    if (HALF) {
+      float q[V], z[V];
+      unpack<T>(pb[i], q);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (r0 + i * at_once >= rows) break;
-      if (!turn) {
-        *reinterpret_cast<uint4*>(dst[i]) = pa[i];
-        continue;
+      for (int j = 0; j < V; ++j) {
+        const float2 f = c[u * V + j];
+        y[j] = p[j] * f.x - q[j] * f.y;
+        z[j] = q[j] * f.x + p[j] * f.y;
       }
-      const float2* c = cs + tok[i] * half;
-      float p[V], y[V];
-      unpack<T>(pa[i], p);
-      if (HALF) {
-        float q[V], z[V];
-        unpack<T>(pb[i], q);
+      *reinterpret_cast<uint4*>(dst[i] + half) = pack<T>(z);
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float2 f = c[u * V + j];
-          y[j] = p[j] * f.x - q[j] * f.y;
-          z[j] = q[j] * f.x + p[j] * f.y;
-        }
-        *reinterpret_cast<uint4*>(dst[i] + half) = pack<T>(z);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float2 f = c[u * (V / 2) + j];
-          y[2 * j] = p[2 * j] * f.x - p[2 * j + 1] * f.y;
-          y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
-        }
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 f = c[u * (V / 2) + j];
+        y[2 * j] = p[2 * j] * f.x - p[2 * j + 1] * f.y;
+        y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
       }
-      *reinterpret_cast<uint4*>(dst[i]) = pack<T>(y);
     }
+    *reinterpret_cast<uint4*>(dst[i]) = pack<T>(y);
   }
 }
 
@@ -181,13 +186,24 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(const RopeArgs a) {
 }
 
 template <typename T>
-jolt_status launch_rope(const RopeArgs& a, bool half, bool vec, cudaStream_t st) {
-  const unsigned grid = unsigned((a.n_tokens + a.tb - 1) / a.tb);
-  const size_t smem = size_t(a.tb) * (a.rot / 2) * sizeof(float2);
+jolt_status launch_rope(RopeArgs a, bool half, bool vec, cudaStream_t st) {
+  const int heads = a.t[0].heads + a.t[1].heads, pairs = a.rot / 2;
   if (vec) {
-    if (half) k_rope_vec<T, true><<<grid, kThreads, smem, st>>>(a);
-    else k_rope_vec<T, false><<<grid, kThreads, smem, st>>>(a);
+    constexpr int V = 16 / sizeof(T);
+    const int units = (half ? pairs : a.rot) / V + (a.d - a.rot) / V, at_once = kThreads / units;
+    // the table of a block's tokens within the shared memory that every launch has
+    a.rows_at = kRows;
+    while (a.rows_at > 1 && (a.rows_at * at_once / heads + 2) * pairs * int(sizeof(float2)) > 48 * 1024) --a.rows_at;
+    a.magic = uint32_t(((uint64_t(1) << 32) + heads - 1) / heads);
+    const int rows = a.rows_at * at_once;
+    const int64_t total = a.n_tokens * heads, grid = (total + rows - 1) / rows;
+    if (grid > 0x7fffffff) return JOLT_ERR_INVALID_ARG;
+    const size_t smem = size_t(std::min<int64_t>(rows / heads + 2, a.n_tokens)) * pairs * sizeof(float2);
+    if (half) k_rope_vec<T, true><<<unsigned(grid), kThreads, smem, st>>>(a);
+    else k_rope_vec<T, false><<<unsigned(grid), kThreads, smem, st>>>(a);
   } else {
+    const unsigned grid = unsigned((a.n_tokens + a.tb - 1) / a.tb);
+    const size_t smem = size_t(a.tb) * pairs * sizeof(float2);
     if (half) k_rope_any<T, true><<<grid, kThreads, smem, st>>>(a);
     else k_rope_any<T, false><<<grid, kThreads, smem, st>>>(a);
   }
