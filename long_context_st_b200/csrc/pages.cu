@@ -67,33 +67,54 @@ struct AppendArgs {
   uint32_t rows;  // of K, and of V
 };
 
-// Eight elements at p as floats.
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight elements as loaded, and as floats.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float* f) const {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          f[4 * i + e] = __uint_as_float(w[e]);
+        } else {
+          f[2 * e] = __uint_as_float(w[e] << 16);
+          f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+      }
+    }
+  }
+};
 
-// Packs this lane's codes and stores them: piece j is B bytes at (j*4 + m)*B of the row.
+// Packs this lane's codes and stores them: piece j is B bytes at (j*4 + m)*B of the row. c: floats
+// 1.5 * 2^23 + code; as bits kBits + code, so that sums of them times 2^(B e) are the codes' fields plus a
+// constant.
 template <int B, int J>
-__device__ __forceinline__ void store_codes(const uint32_t (&c)[8 * J], uint8_t* row, int m) {
+__device__ __forceinline__ void store_codes(const float (&c)[8 * J], uint8_t* row, int m) {
+  constexpr uint32_t kBits = 0x4B400000u;
+  constexpr int P = B == 8 ? 4 : 8;  // codes of a word (or half word)
+  uint32_t base = 0;
+#pragma unroll
+  for (int e = 0; e < P; ++e) base += kBits << (e * B);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    uint32_t w[B == 8 ? 2 : 1];
+    uint32_t w[8 / P];
 #pragma unroll
-    for (int i = 0; i < (B == 8 ? 2 : 1); ++i) {
+    for (int i = 0; i < 8 / P; ++i) {
       w[i] = 0;
 #pragma unroll
-      for (int e = 0; e < (B == 8 ? 4 : 8); ++e) w[i] |= c[8 * j + 4 * i + e] << (e * B);
+      for (int e = P - 1; e >= 0; --e) w[i] = (w[i] << B) + __float_as_uint(c[8 * j + P * i + e]);
+      w[i] -= base;
     }
     uint8_t* dst = row + (j * 4 + m) * B;
     if constexpr (B == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
@@ -102,13 +123,25 @@ __device__ __forceinline__ void store_codes(const uint32_t (&c)[8 * J], uint8_t*
   }
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Rotate, quantise and pack rows as they are written. The arithmetic is jolt_rotate_rows then
 // jolt_quantize_pack, operation by operation (butterflies over strides 1, 2, .. D/2 in that order, the
 // same roundings), so the codes are theirs bit for bit. The quotient a / scale is taken as
 // a * fl(1 / scale): with both roundings it is within 1.5 * 2^-23 |q| of the exact quotient and the
 // rounded one within 2^-24 |q|, so for |q| < levels + 1/2 both round to the same whole number unless
-// the product lies within levels * 2^-20 of a half-integer; only then is the division done. The
-// product is first clipped to (-1/2, levels + 1/2), where clipping and rounding commute.
+// the product lies within levels * 2^-21 of a half-integer (2^-22 |q| would do). A warp where some element does, or where some
+// product leaves (-1/2, levels + 1/2) and has to be clipped (the extremes' products tell), takes the
+// division for all of its rows; on Gaussian rows that is one warp in 70 at 4 bits, one in 5 at 8.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
   constexpr int J = D / 32, N = 8 * J;  // pieces and elements of a lane
@@ -119,12 +152,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
   const int bits = kv ? a.p.bv : a.p.bk;
   const float levels = float((1 << bits) - 1);
   const uint32_t step = gridDim.x * kWarps * 8;
-  for (uint32_t base = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * 8; base < a.rows; base += step) {
-    const uint32_t r = base + g;
-    // where the row comes from and goes to; a row that is not written runs along on zeros
+  // where row r comes from (loaded) and goes to; a row that is not written runs along on zeros
+  Raw8<T> raw[J];
+  uint8_t* page_base;
+  int row;
+  auto fetch = [&](uint32_t r) {
     const T* x = nullptr;
-    uint8_t* page_base = nullptr;
-    int row = 0;
+    page_base = nullptr;
+    row = 0;
     if (r < a.rows) {
       const uint32_t bi = r / uint32_t(a.p.n_kv), b = bi / uint32_t(a.n_new);
       const int h = int(r - bi * a.p.n_kv), i = int(bi - b * a.n_new);
@@ -143,16 +178,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
         }
       }
     }
-    float v[N];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      if (x) {
-        load8(x + piece_at(j, m), v + 8 * j);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * j + e] = 0.f;
-      }
+      if (x) raw[j].load(x + piece_at(j, m));
+      else raw[j].zero();
     }
+  };
+  uint32_t base = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * 8;
+  if (base < a.rows) fetch(base + g);
+  for (; base < a.rows; base += step) {
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < J; ++j) raw[j].floats(v + 8 * j);
+    uint8_t* const to_page = page_base;
+    const int to_row = row;
+    // the next rows arrive while these are worked on
+    if (base + step < a.rows) fetch(base + step + g);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) ^ ((neg << (31 - i)) & 0x80000000u));
     // stride 1 inside the packed pairs, then 2 and 4 on pairs
@@ -192,53 +233,54 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
           y[i + s] = f2_fma(q, minus, p);
         }
     const f2 isd2 = f2_make(isd, isd);
-    float lo = INFINITY, hi = -INFINITY, bad = 0.f;
+    float lo = INFINITY, hi = -INFINITY;  // NaN when some element is
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       y[i] = f2_mul(y[i], isd2);
       const float2 t = f2_get(y[i]);
-      lo = fminf(lo, fminf(t.x, t.y));
-      hi = fmaxf(hi, fmaxf(t.x, t.y));
-      bad = fmaf(t.x, 0.f, fmaf(t.y, 0.f, bad));
+      lo = min_nan(lo, min_nan(t.x, t.y));
+      hi = max_nan(hi, max_nan(t.x, t.y));
     }
 #pragma unroll
     for (int s = 1; s <= 2; s <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, s));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, s));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, s));
     }
     const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), levels)), hz = __float2half_rn(lo);
     const float sc = __half2float(hs), zero = __half2float(hz);
+    const bool numeric = !(fabsf(sc) < INFINITY) || !(fabsf(zero) < INFINITY);
     const float rs = sc != 0.f ? __frcp_rn(sc) : 0.f;
-    const f2 mz = f2_make(-zero, -zero), rs2 = f2_make(rs, rs);
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-    const float top = levels + 0.4375f, margin = 0.5f - levels * 9.5367431640625e-7f;
-    uint32_t c[N], ties = 0;
+    float c[N], off = 0.f;
+    {
+      const f2 mz = f2_make(-zero, -zero), rs2 = f2_make(rs, rs), up = f2_make(kMagic, kMagic), down = f2_make(-kMagic, -kMagic);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const float2 q = f2_get(f2_mul(f2_add(y[i], mz), rs2));
-      const float q0 = fminf(fmaxf(q.x, -0.4375f), top), q1 = fminf(fmaxf(q.y, -0.4375f), top);
-      const float r0 = q0 + kMagic, r1 = q1 + kMagic;
-      c[2 * i] = __float_as_uint(r0) & 0xFFu;
-      c[2 * i + 1] = __float_as_uint(r1) & 0xFFu;
-      if (fabsf(q0 - (r0 - kMagic)) >= margin) ties |= 1u << (2 * i);
-      if (fabsf(q1 - (r1 - kMagic)) >= margin) ties |= 1u << (2 * i + 1);
+      for (int i = 0; i < N / 2; ++i) {
+        const f2 q = f2_mul(f2_add(y[i], mz), rs2);
+        const f2 r = f2_add(q, up);
+        const float2 d = f2_get(f2_fma(f2_add(r, down), minus, q)), t = f2_get(r);
+        c[2 * i] = t.x;
+        c[2 * i + 1] = t.y;
+        off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+      }
     }
-    if (ties) {
+    const float q_lo = (lo - zero) * rs, q_hi = (hi - zero) * rs;
+    const bool plain = off < 0.5f - levels * 4.76837158203125e-7f && q_lo > -0.4375f && q_hi < levels + 0.4375f;
+    if (!__all_sync(0xffffffffu, plain)) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if ((ties >> i) & 1) {
-          const float2 t = f2_get(y[i >> 1]);
-          const float q = rintf(__fdiv_rn(__fsub_rn((i & 1) ? t.y : t.x, zero), sc));
-          c[i] = uint32_t(fminf(fmaxf(q, 0.f), levels));
-        }
+      for (int i = 0; i < N; ++i) {
+        const float2 t = f2_get(y[i >> 1]);
+        float q = 0.f;
+        if (sc != 0.f) q = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn((i & 1) ? t.y : t.x, zero), sc)), 0.f), levels);
+        c[i] = q + kMagic;
+      }
     }
-    const bool numeric = !(bad == 0.f) || !(fabsf(sc) < INFINITY) || !(fabsf(zero) < INFINITY);
-    if (page_base) {
-      uint8_t* dst = page_base + (kv ? a.p.vc : a.p.kc) + int64_t(row) * (D * bits / 8);
+    if (to_page) {
+      uint8_t* dst = to_page + (kv ? a.p.vc : a.p.kc) + int64_t(to_row) * (D * bits / 8);
       if (bits == 4) store_codes<4, J>(c, dst, m);
       else if (bits == 8) store_codes<8, J>(c, dst, m);
       else store_codes<2, J>(c, dst, m);
-      if (m == 0) reinterpret_cast<__half2*>(page_base + (kv ? a.p.vs : a.p.ks))[row] = __halves2half2(hs, hz);
+      if (m == 0) reinterpret_cast<__half2*>(to_page + (kv ? a.p.vs : a.p.ks))[to_row] = __halves2half2(hs, hz);
       if (numeric) report_error(a.err, JOLT_ERR_NUMERIC);
     }
   }

@@ -157,8 +157,8 @@ def test_attention_refusals():
 
 
 def test_quotient_by_reciprocal_gives_the_divisions_codes():
-    """jolt_pages_append's quotient: clip(a fl(1/s)) rounded, the division only within levels * 2^-20 of a
-    half-integer, against clip(rint(a / s)), in float32, near-ties planted one and two ulps either side."""
+    """jolt_pages_append's quotient: a fl(1/s) rounded, the division only within levels * 2^-21 of a
+    half-integer or where it has to be clipped, against clip(rint(a / s)), in float32, near-ties planted one and two ulps either side."""
     f32, rng = np.float32, np.random.default_rng(12)
     for levels in (3, 15, 255):
         s = np.concatenate([rng.uniform(1e-4, 4.0, 300000), 2.0 ** rng.uniform(-24, 15, 100000)]).astype(np.float16)
@@ -168,10 +168,11 @@ def test_quotient_by_reciprocal_gives_the_divisions_codes():
         up, down = np.nextafter(tie, f32(np.inf)), np.nextafter(tie, f32(-np.inf))
         some = (rng.uniform(-0.7, levels + 0.7, s.size).astype(f32) * s).astype(f32)
         for a in (some, tie, up, down, np.nextafter(up, f32(np.inf)), np.nextafter(down, f32(-np.inf)), (some * f32(1e4)).astype(f32)):
-            q = np.clip((a * (f32(1) / s).astype(f32)).astype(f32), f32(-0.4375), f32(levels) + f32(0.4375))
+            q = (a * (f32(1) / s).astype(f32)).astype(f32)
             c = np.rint(q)
-            near = np.abs((q - c).astype(f32)) >= f32(0.5) - f32(levels) * f32(2.0 ** -20)
+            near = np.abs((q - c).astype(f32)) >= f32(0.5) - f32(levels) * f32(2.0 ** -21)
+            out = (q <= f32(-0.4375)) | (q >= f32(levels) + f32(0.4375))
             want = np.clip(np.rint((a / s).astype(f32)), 0, levels)
-            got = np.where(near, want, c)
+            got = np.where(near | out, want, c)
             assert np.array_equal(np.abs(got), want)
             assert near.mean() < 1e-3 or a is not some
