@@ -504,65 +504,80 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
 }
 
 // One warp a row: joins the splits, rotates their sum back, then adds the drafted tokens' part and the
-// prefix. Launched while k_tree still runs (its grid starts as k_tree's blocks leave); it waits for
-// k_tree's end before it reads anything.
+// prefix. Launched while k_tree still runs (its blocks start as k_tree's leave room); what k_tree does not
+// write is read at once, the rest after k_tree's end, all of it in one go.
 template <typename T, int D, int TILE>
 __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  float back[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) back[e] = rsqrtf(float(D)) * rot_sign(a.p.seed, lane * E + e);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= int64_t(a.batch) * a.n_new * a.n_q) return;
   const int64_t bi = row / a.n_q;
   const int b = int(bi / a.n_new), i = int(bi % a.n_new);
-  if (i >= draft_count(a, b)) return;
+  const bool mine = i < draft_count(a, b);
   const int splits = splits_of<TILE>(a, b, lane);
+  if (!mine) return;
+  float back[E], po[E];
+  float pre = -INFINITY;
+  if (a.prefix_lse) pre = a.prefix_lse[row] * 1.4426950408889634f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    back[e] = rsqrtf(float(D)) * rot_sign(a.p.seed, lane * E + e);
+    po[e] = 0.f;
+  }
+  if (pre != -INFINITY) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) po[e] = ld_as_float(static_cast<const T*>(a.prefix_out) + row * D + lane * E, e);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* acc = a.acc + row * a.parts * D + lane * E;
+  auto part = [&](int s, float (&x)[E]) {
+    if constexpr (E == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(acc + int64_t(s) * D);
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(acc + int64_t(s) * D);
+      x[0] = y.x, x[1] = y.y;
+    }
+  };
+  constexpr int kBatch = 8;  // splits whose loads are in flight together
+  float x[kBatch][E], xd[E];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+    if (k < splits) part(k, x[k]);
+  if (draft) part(a.splits, xd);
   float2 p[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int s = lane + 32 * x;
+  for (int k = 0; k < 2; ++k) {
+    const int s = lane + 32 * k;
     const bool there = s < splits || (draft && s == a.splits);
-    p[x] = there ? a.ml[row * a.parts + s] : make_float2(-INFINITY, 0.f);
+    p[k] = there ? a.ml[row * a.parts + s] : make_float2(-INFINITY, 0.f);
   }
-  const float pre = a.prefix_lse ? a.prefix_lse[row] * 1.4426950408889634f : -INFINITY;
   const float top = fmaxf(warp_max(fmaxf(p[0].x, p[1].x)), pre);
   const float ref = top == -INFINITY ? 0.f : top;
   float w[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) w[x] = exp2f(p[x].x - ref);
+  for (int k = 0; k < 2; ++k) w[k] = exp2f(p[k].x - ref);
   const float wp = pre == -INFINITY ? 0.f : exp2f(pre - ref);
   const float sum = warp_sum(w[0] * p[0].y + w[1] * p[1].y) + wp;
   float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const float* acc = a.acc + row * a.parts * D + lane * E;
-  constexpr int kBatch = 8;  // splits whose loads are in flight together
-  for (int s0 = 0; s0 < splits; s0 += kBatch) {
-    float f[kBatch], x[kBatch][E];
+  for (int s0 = 0;;) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int s = s0 + i;
-      f[i] = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
-      if (s >= splits) f[i] = 0.f;
+    for (int k = 0; k < kBatch; ++k) {
+      const int s = s0 + k;
+      const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
+      if (s < splits && f != 0.f) {  // a split that saw nothing has left nothing
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
-      if (f[i] != 0.f) {  // a split that saw nothing has left nothing
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(acc + int64_t(s) * D);
-          x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(acc + int64_t(s) * D);
-          x[i][0] = y.x, x[i][1] = y.y;
-        }
+        for (int e = 0; e < E; ++e) o[e] += f * x[k][e];
       }
     }
+    s0 += kBatch;
+    if (s0 >= splits) break;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f[i] * x[i][e];
+    for (int k = 0; k < kBatch; ++k)
+      if (s0 + k < splits) part(s0 + k, x[k]);
   }
   if (a.perm) {
     __shared__ float row_s[4][D];
@@ -580,13 +595,12 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
     const float f = __shfl_sync(0xffffffffu, a.splits < 32 ? w[0] : w[1], a.splits & 31);
     if (f != 0.f) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * acc[int64_t(a.splits) * D + e];
+      for (int e = 0; e < E; ++e) o[e] += f * xd[e];
     }
   }
   if (wp != 0.f) {
-    const T* po = static_cast<const T*>(a.prefix_out) + row * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += wp * ld_as_float(po, e);
+    for (int e = 0; e < E; ++e) o[e] += wp * po[e];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   T* out = static_cast<T*>(a.out) + row * D + lane * E;

@@ -696,6 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[i][e] = __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
     }
+    for (int i = threadIdx.x; i < (kRows - rows) * (D / 8) * 2; i += kThreads) {
+      const int r = rows + i / (D / 4), at16 = i % (D / 4);  // 16-byte places of a row, both terms (any order)
+      *reinterpret_cast<uint4*>(smem + S::q + (at16 >> 3) * S::kChunk + r * 128 + (at16 & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    for (int r = rows + threadIdx.x; r < kRows; r += kThreads) reinterpret_cast<float*>(smem + S::qs)[r] = 0.f;
     int at[E];
     float sign[E], low[E];  // low: 2^-(a code field's place in its byte)
 #pragma unroll
@@ -707,10 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = warp + i * kW;
+      if (r >= rows) break;  // rows past the last are zeros
 #pragma unroll
       for (int e = 0; e < E; ++e) v[i][e] *= sign[e];
       // the elements of H x add up to D x_0
-      if (lane == 0 && r < kRows) reinterpret_cast<float*>(smem + S::qs)[r] = v[i][0] * (float(D) * isd);
+      if (lane == 0) reinterpret_cast<float*>(smem + S::qs)[r] = v[i][0] * (float(D) * isd);
       warp_fwht<E>(v[i]);
       float most = 0.f;
 #pragma unroll
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = warp + i * kW;
-      if (r >= kRows) break;
+      if (r >= rows) break;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float x = v[i][e] * up * low[e];
