@@ -420,7 +420,8 @@ jolt_status jolt_decode_attn_noalloc(const jolt_shape* shape, const jolt_cell_ch
  * Device-side checks: a length outside [0, max_pages*page_size] is clamped, a table entry outside
  * [0, n_pages) makes its page's tokens invisible (reads, attention) or unwritten (append); both
  * set JOLT_ERR_INVALID_ARG in the error word. err (device int32, may be NULL) as in
- * jolt_quantize_pack: set, never cleared. A call with batch, n_new or n_out 0 returns JOLT_OK. */
+ * jolt_quantize_pack: set, never cleared. batch is at most 65535; a call
+ * with batch, n_new or n_out 0 returns JOLT_OK. */
 typedef struct {
   int32_t n_pages;      /* pages in the pool >= 1 */
   int32_t page_size;    /* tokens per page: 16, 32, 64 or 128 */
@@ -458,7 +459,8 @@ jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, const int32_t
  * lens[s], into row i of k_out and v_out; other rows are left as they were.
  *   start    device int32 [batch] >= 0 (NULL: 0; a negative one is an error and reads nothing)
  *   k_out, v_out  device [batch][n_kv][n_out][d_h] io dtype, rows contiguous, element strides stride_b
- *            (sequence) and stride_h (head), multiples of 8, 16-byte aligned; either may be NULL. With a
+ *            (sequence) and stride_h (head), multiples of 8 and at least n_out*d_h (where there are
+ *            several), 16-byte aligned; either may be NULL. With a
  *            layer's strides of jolt_compress's K and V this folds a tail into a stored cache's input.
  * Asynchronous on `stream`. */
 jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
@@ -492,7 +494,8 @@ size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t 
  *   lse      device fp32 [batch][n_new][n_q], or NULL
  *   ws       device, >= jolt_tree_attn_workspace, 256-byte aligned, its first 4 bytes zero before the
  *            first call (the error word, read by jolt_check); calls sharing a ws must not overlap in time
- * Scores and softmax statistics are fp32. Asynchronous on `stream`. */
+ * Scores and softmax statistics are fp32. bf16 with more than 32 query rows (n_new * n_q / n_kv) runs its
+ * products on tcgen05, the rest on m16n8k16 MMAs. Asynchronous on `stream`. */
 jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
                            const int32_t* lens, int32_t batch, int32_t n_new, int32_t n_q, const int32_t* counts,
                            const uint64_t* mask, const void* q, int64_t q_stride_b, int64_t q_stride_t,

@@ -542,7 +542,7 @@ def tree_attn(p: Pages, pool, table, lens, q, out, ws, k=None, v=None, mask=None
 
 def rope(q, k, pos, inv_freq, q_out=None, k_out=None, layout="half", scaling=1.0, inverse=False, stream=None):
     """Rotary positions of q [n_tokens, n_q, d_h] and k [n_tokens, n_kv, d_h] (either may be None) into
-    q_out and k_out (default: new tensors; q_out may be q). pos int32 [n_tokens]; inv_freq fp32
+    q_out and k_out (default: new tensors, on the current stream only; q_out may be q). pos int32 [n_tokens]; inv_freq fp32
     [rot_dim / 2]: the first rot_dim elements of each head are rotated. inverse: the transpose, the
     gradient of the forward call. Returns (q_out, k_out)."""
     dev = _device()
@@ -563,6 +563,8 @@ def rope(q, k, pos, inv_freq, q_out=None, k_out=None, layout="half", scaling=1.0
             _bad(f"{what} [n_tokens, heads, d_h] is wanted")
         h = x.shape[1]
         if y is None:
+            if stream is not None:  # memory of the current stream, written on another
+                _bad(f"{what}_out is wanted with a stream")
             y = torch.empty((n, h, d), dtype=dt, device=x.device)
         args += [_dev(x, dt, (n, h, d), what, dev, 2), _dev(y, dt, (n, h, d), what + "_out", dev, 2), h,
                  x.stride(0) if n > 1 else h * d, y.stride(0) if n > 1 else h * d]

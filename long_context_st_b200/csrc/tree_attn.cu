@@ -10,6 +10,9 @@
 // further power of two), so codes feed m16n8k16 MMAs after one mask a pair. The places' powers are taken
 // from R q (keys) and from the outputs (values); o and the zeros enter through sums: o sum(R q) in the
 // scores, and for the values a further MMA row of ones, which adds up p * scale exactly as rounded.
+// The MMA aligns a subnormal's product by f16's least exponent, which costs the sum about 10 - b bits of its
+// 24: against 64 bits the outputs of fp32 were off by 5e-6 (8 bits) to 3e-4 (2 bits), and the log-sum-exp
+// of 2-bit keys by 3e-6. So fp32, and 2-bit keys, take one more operation a pair: c - o as normal numbers.
 // What is rounded is the other operand: R q is carried as two f16 terms (22 bits: the log-sum-exp stays
 // fp32-accurate), p * scale as one f16 term for bf16 output (11 bits, against the 8 the output keeps) and
 // as two for fp32. Both are first scaled by powers of two into f16's normal range: R q by the block's
@@ -30,12 +33,17 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;        // tokens a warp takes at a time
 constexpr int kMaxSplits = 63;   // + the drafted tokens' own partial: two per lane in the merge
 constexpr int kMaxStages = 4;
-constexpr float kRoom = 4.f;    // how far above a row's maximum its reference is set
-constexpr float kMost = 256.f;  // most that a thread's p of a tile may add up to
-constexpr int kPExp = 7;        // p * scale is carried times 2^(7 - ve): below 2^15
+// References (see k_tree): room above a row's maximum when one is set, what a thread's four p of a tile may add
+// up to, and the power of two p * scale is carried with (times 2^-ve), so that it stays below 2^15. fp32
+// output takes less room: its second f16 term of p * scale must not run out of f16's range below.
+template <typename T>
+struct Ref {
+  static constexpr float room = sizeof(T) == 4 ? 1.f : 4.f, most = sizeof(T) == 4 ? 8.f : 256.f;
+  static constexpr int p_exp = sizeof(T) == 4 ? 12 : 7;
+};
 
 // Keys of one tile: acc[grp][nt] += fields (tokens grp*16 + {g, g+8}) x R q (columns of tile nt).
-template <int D, int B, int NT, int QT>
+template <int D, int B, int NT, int QT, bool NORMAL>
 __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, int lane, float (&s)[2][NT][4]) {
   constexpr int W = D * B / 128;  // words of a lane's quarter row
   const int g = lane >> 2, m = lane & 3;
@@ -47,10 +55,10 @@ __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, in
     uint32_t a0[4], a1[4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      a0[2 * x] = field_pair<B, W>(w[0], 2 * st + x);
-      a0[2 * x + 1] = field_pair<B, W>(w[1], 2 * st + x);
-      a1[2 * x] = field_pair<B, W>(w[2], 2 * st + x);
-      a1[2 * x + 1] = field_pair<B, W>(w[3], 2 * st + x);
+      a0[2 * x] = NORMAL ? code_pair<B, W>(w[0], 2 * st + x) : field_pair<B, W>(w[0], 2 * st + x);
+      a0[2 * x + 1] = NORMAL ? code_pair<B, W>(w[1], 2 * st + x) : field_pair<B, W>(w[1], 2 * st + x);
+      a1[2 * x] = NORMAL ? code_pair<B, W>(w[2], 2 * st + x) : field_pair<B, W>(w[2], 2 * st + x);
+      a1[2 * x + 1] = NORMAL ? code_pair<B, W>(w[3], 2 * st + x) : field_pair<B, W>(w[3], 2 * st + x);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -64,8 +72,8 @@ __device__ __forceinline__ void keys_tile(const uint8_t* kc, const uint2* qf, in
 }
 
 // Values of one tile: o[mt][nt] += fields^T (features) x (p scale) (tokens), PT terms of the latter; o[D / 16]
-// the sum of p scale (a row of ones).
-template <int D, int B, int NT, int PT>
+// the sum of p scale (a row of ones; not with NORMAL, whose codes are centred).
+template <int D, int B, int NT, int PT, bool NORMAL>
 __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&pf)[PT][2][NT][2], int lane,
                                             float (&o)[D / 16 + 1][NT][4]) {
   constexpr int CB = D * B / 64;             // bytes of a lane's eighth row
@@ -82,12 +90,12 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
       else load_words<W>(src, w[r]);
     }
 #pragma unroll
-    for (int mt = 0; mt <= D / 16; ++mt) {
+    for (int mt = 0; mt < D / 16 + (NORMAL ? 0 : 1); ++mt) {
       uint32_t a[4];
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        a[f] = mt < D / 16 ? field_across<B, W>(w[0], w[1], 2 * mt + f) : ones[f];
-        a[f + 2] = mt < D / 16 ? field_across<B, W>(w[2], w[3], 2 * mt + f) : ones[f];
+        a[f] = mt == D / 16 ? ones[f] : NORMAL ? code_across<B, W>(w[0], w[1], 2 * mt + f) : field_across<B, W>(w[0], w[1], 2 * mt + f);
+        a[f + 2] = mt == D / 16 ? ones[f] : NORMAL ? code_across<B, W>(w[2], w[3], 2 * mt + f) : field_across<B, W>(w[2], w[3], 2 * mt + f);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -110,6 +118,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   constexpr int QT = PACK ? 1 : 2;
   constexpr int PT = !PACK && sizeof(T) == 4 ? 2 : 1;
   constexpr int E = D / 32, NS = D / 16, C = 8 * NT;
+  constexpr bool kWhole = sizeof(T) == 4;       // codes as normal numbers
+  const bool k_whole = kWhole || a.p.bk == 2;  // keys' codes
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, m = lane & 3;
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
     __syncthreads();
     int k = 0;  // 2^k top in [2^14, 2^15)
     if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
-    unscale = pow2i(24 - k);
+    unscale = pow2i((k_whole ? 0 : 24) - k);
     const int lnc = log2_codes(a.p.bk), half = 1 << (lnc - 1);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
       const int mm = f / (D / 4), fq = f % (D / 4);       // quarter row, feature in it
       const int c = fq & (2 * half - 1);                  // code in its word
       const int pair = ((fq >> lnc) << (lnc - 1)) + (c & (half - 1)), hi = c >> (lnc - 1);
-      const float up = pow2i(k - ((a.p.bk * pair) & 7));  // less the field's place in its byte
+      const float up = pow2i(k - (k_whole ? 0 : (a.p.bk * pair) & 7));  // less the field's place in its byte
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int r = warp + i * kWarps;
@@ -250,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   }
   __syncthreads();
 
-  // A column's (query row's) reference is a whole number, 4 above its maximum when it was last set; it is set
-  // anew only when a thread's four p of a tile add up to more than 2^8, so the usual tile takes no maximum.
+  // A column's (query row's) reference is a whole number, some room above its maximum when it was last set; it
+  // is set anew only when a thread's four p of a tile add up to too much, so the usual tile takes no maximum.
   float o[NS + 1][NT][4], ref[NT][2], l[NT][2], z[NT][2], cqs[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -267,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
       for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.f;
   }
   int ve = -30;            // value scales met so far are below 2^ve
-  float v_lim = pow2i(ve), v_up = pow2i(kPExp - ve);
-  const float ov_off = float(1 << (a.p.bv - 1));
+  float v_lim = pow2i(ve), v_up = pow2i(Ref<T>::p_exp - ve);
+  const float ov_off = float(1 << (a.p.bv - 1)), ok_off = k_whole ? float(1 << (a.p.bk - 1)) : 0.f;
   for (int n = 0, st = 0, par = 0; n < n_mine; ++n) {
     if (!wait_all(bar0 + 8 * st, par, a.err)) {
       // gave up (reported): wait, with the same limit, for what is still in flight, then stop
@@ -299,9 +309,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[grp][nt][c] = 0.f;
-      if (a.p.bk == 4) keys_tile<D, 4, NT, QT>(kc, qf, lane, s);
-      else if (a.p.bk == 8) keys_tile<D, 8, NT, QT>(kc, qf, lane, s);
-      else keys_tile<D, 2, NT, QT>(kc, qf, lane, s);
+      if (a.p.bk == 4) keys_tile<D, 4, NT, QT, kWhole>(kc, qf, lane, s);
+      else if (a.p.bk == 8) keys_tile<D, 8, NT, QT, kWhole>(kc, qf, lane, s);
+      else keys_tile<D, 2, NT, QT, true>(kc, qf, lane, s);
       if (PACK) {  // the two terms of R q
 #pragma unroll
         for (int grp = 0; grp < 2; ++grp)
@@ -313,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 kf = __half22float2(ksz[8 * i]), vf = __half22float2(vsz[8 * i]);
-        const float ks = kf.x * unscale;
+        const float ks = kf.x * unscale, kz = kf.y + ok_off * kf.x;
         vsc[i] = vf.x;
         vze[i] = vf.y + ov_off * vf.x;
         if (!whole && (unseen >> i & 1)) vsc[i] = vze[i] = 0.f;
@@ -323,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float& x = s[i >> 1][nt][2 * (i & 1) + c];
-            x = x * ks + kf.y * cqs[nt][c];
+            x = x * ks + kz * cqs[nt][c];
           }
       }
       if (anew) {
@@ -332,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         const float drop = pow2i(max(ve - ve_new, -126));
         ve = ve_new;
         v_lim = pow2i(min(ve, 127));
-        v_up = pow2i(kPExp - ve);
+        v_up = pow2i(Ref<T>::p_exp - ve);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
               if (!(unseen >> i & 1)) t = fmaxf(t, s[i >> 1][nt][2 * (i & 1) + c]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-            const float now = fmaxf(ref[nt][c], ceilf(t) + kRoom);
+            const float now = fmaxf(ref[nt][c], ceilf(t) + Ref<T>::room);
             const float f = now == ref[nt][c] ? 1.f : ex2(ref[nt][c] - now);
             ref[nt][c] = now;
             l[nt][c] *= f;
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           sum[nt][c] = (s[0][nt][c] + s[0][nt][c + 2]) + (s[1][nt][c] + s[1][nt][c + 2]);
           most = fmaxf(most, sum[nt][c]);
         }
-      if (anew || !__any_sync(0xffffffffu, most > kMost || v_top > v_lim)) break;
+      if (anew || !__any_sync(0xffffffffu, most > Ref<T>::most || v_top > v_lim)) break;
     }
     uint32_t pf[PT][2][NT][2];
 #pragma unroll
@@ -412,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
           }
           pf[0][grp][nt][i] = trans8x8(hi);
         }
-    if (a.p.bv == 4) values_tile<D, 4, NT, PT>(vc, pf, lane, o);
-    else if (a.p.bv == 8) values_tile<D, 8, NT, PT>(vc, pf, lane, o);
-    else values_tile<D, 2, NT, PT>(vc, pf, lane, o);
+    if (a.p.bv == 4) values_tile<D, 4, NT, PT, kWhole>(vc, pf, lane, o);
+    else if (a.p.bv == 8) values_tile<D, 8, NT, PT, kWhole>(vc, pf, lane, o);
+    else values_tile<D, 2, NT, PT, kWhole>(vc, pf, lane, o);
     __syncwarp();  // every lane is done with the stage
     if (n + a.stages < n_mine) fetch(st);
     if (++st == a.stages) {
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
     }
   __syncthreads();
   // fields' powers of two, and o sum(p scale), out of the outputs
-  const float unit = pow2i(ve - kPExp);
+  const float unit = pow2i(ve - Ref<T>::p_exp);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -452,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         xz[warp * C + col] = z[nt][c] * f;
       }
       ref[nt][c] = top;
-      const float off = ov_off * o[NS][nt][c];
+      const float off = kWhole ? 0.f : ov_off * o[NS][nt][c];
 #pragma unroll
       for (int mt = 0; mt < NS; ++mt) {
-        o[mt][nt][c] = (o[mt][nt][c] * pow2i(24 - ((2 * mt * a.p.bv) & 7)) - off) * (f * unit);
-        o[mt][nt][c + 2] = (o[mt][nt][c + 2] * pow2i(24 - (((2 * mt + 1) * a.p.bv) & 7)) - off) * (f * unit);
+        o[mt][nt][c] = (o[mt][nt][c] * (kWhole ? 1.f : pow2i(24 - ((2 * mt * a.p.bv) & 7))) - off) * (f * unit);
+        o[mt][nt][c + 2] = (o[mt][nt][c + 2] * (kWhole ? 1.f : pow2i(24 - (((2 * mt + 1) * a.p.bv) & 7))) - off) * (f * unit);
         if (PACK) {
           o[mt][nt][c] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c], 2);
           o[mt][nt][c + 2] += __shfl_xor_sync(0xffffffffu, o[mt][nt][c + 2], 2);
@@ -511,15 +521,13 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= int64_t(a.batch) * a.n_new * a.n_q) return;
-  const int64_t bi = row / a.n_q;
+  const int64_t rows = int64_t(a.batch) * a.n_new * a.n_q, bi = (row < rows ? row : 0) / a.n_q;
   const int b = int(bi / a.n_new), i = int(bi % a.n_new);
-  const bool mine = i < draft_count(a, b);
+  const bool mine = row < rows && i < draft_count(a, b);
   const int splits = splits_of<TILE>(a, b, lane);
-  if (!mine) return;
   float back[E], po[E];
   float pre = -INFINITY;
-  if (a.prefix_lse) pre = a.prefix_lse[row] * 1.4426950408889634f;
+  if (mine && a.prefix_lse) pre = a.prefix_lse[row] * 1.4426950408889634f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     back[e] = rsqrtf(float(D)) * rot_sign(a.p.seed, lane * E + e);
@@ -529,7 +537,9 @@ __global__ void __launch_bounds__(128) k_tree_merge(const TreeArgs a, bool draft
 #pragma unroll
     for (int e = 0; e < E; ++e) po[e] = ld_as_float(static_cast<const T*>(a.prefix_out) + row * D + lane * E, e);
   }
+  // every block waits, so that this grid never ends before k_tree
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
   const float* acc = a.acc + row * a.parts * D + lane * E;
   auto part = [&](int s, float (&x)[E]) {
     if constexpr (E == 4) {

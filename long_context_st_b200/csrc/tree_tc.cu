@@ -142,7 +142,8 @@ __device__ __forceinline__ void widen_keys(const uint32_t (&w)[4][D * B / 128], 
     for (int i = 0; i < D / 32; ++i) {
       uint32_t h[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) h[x] = field_pair<B, D * B / 128>(w[it], 4 * i + x);
+      for (int x = 0; x < 4; ++x)
+        h[x] = B == 2 ? code_pair<B, D * B / 128>(w[it], 4 * i + x) : field_pair<B, D * B / 128>(w[it], 4 * i + x);
       *reinterpret_cast<uint4*>(tile + off[i] + it * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
@@ -268,7 +269,7 @@ template <int D>
 __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
   using S = Smem<D>;
   const int ps = 1 << a.p.ps_log2;
-  const float vtop = float((1 << a.p.bv) - 1);
+  const float vtop = float((1 << a.p.bv) - 1), ko = a.p.bk == 2 ? 2.f : 0.f;
   const uint32_t at = (uint32_t(c.h) * ps + ((lane * 4) & (ps - 1))) * 4;
   int id = -1, seen = 0;
   uint4 kz, vz;
@@ -300,7 +301,7 @@ __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
       const float2 k = h2_floats(ku[i]), v = h2_floats(vu[i]);
       const bool here = (seen >> i) & 1;
       sc[i] = here ? k.x * c.unscale : 0.f;
-      ze[i] = here ? k.y : 0.f;
+      ze[i] = here ? k.y + ko * k.x : 0.f;
       if (here) most = fmaxf(most, fmaxf(fabsf(v.y), fabsf(v.y + vtop * v.x)));
     }
     float4* dst = reinterpret_cast<float4*>(c.smem + S::sc + q * 1024) + lane * 2;
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
     for (int e = 0; e < E; ++e) {
       at[e] = place_of(lane * E + e, log2_codes(a.p.bk), D);
       sign[e] = rot_sign(a.p.seed, lane * E + e) * a.scale2;
-      low[e] = pow2i(-(a.p.bk * ((at[e] & 7) >> 1) & 7));  // b (pair % (8 / b)) = (b pair) % 8
+      low[e] = a.p.bk == 2 ? 1.f : pow2i(-(a.p.bk * ((at[e] & 7) >> 1) & 7));  // b (pair % (8 / b)) = (b pair) % 8
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
     for (int i = 0; i < kW; ++i) top = fmaxf(top, reinterpret_cast<const float*>(smem + S::rs)[i]);
     int k = 0;
     if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
-    c.unscale = pow2i(24 - k);
+    c.unscale = pow2i((a.p.bk == 2 ? 0 : 24) - k);
     const float up = pow2i(k);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {

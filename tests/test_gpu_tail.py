@@ -99,6 +99,35 @@ def test_rope_gradient_against_differences(cuda_ok, layout):
     assert np.abs(f64(grad) - num).max() <= 2.0 ** -20 * 2 * np.abs(f64(w)).max()
 
 
+def test_python_refusals(cuda_ok):
+    """What the tensors themselves give away: types, shapes, strides, devices."""
+    f = torch.ones(32, device="cuda")
+    q, pos = torch.zeros(3, 4, 64, device="cuda"), i32([0, 1, 2])
+    p = api.make_pages(4, 16, 2, 64, 4, 4, io_dtype="f32")
+    pool, table, lens = api.new_pool(p), i32([[0, 1], [2, 3]]), i32([0, 0])
+    k = torch.zeros(2, 3, 2, 64, device="cuda")
+    out, ws = torch.zeros(2, 3, 4, 64, device="cuda"), api.new_tree_workspace(p, 2, 3, 4, 2)
+    q4 = out.clone()
+    side = torch.cuda.Stream().cuda_stream
+    for call in (lambda: api.rope(q.double(), None, pos, f), lambda: api.rope(q.cpu(), None, pos, f),
+                 lambda: api.rope(q, None, pos.long(), f), lambda: api.rope(q, None, pos[:2], f),
+                 lambda: api.rope(q.transpose(1, 2), None, pos, f), lambda: api.rope(q, None, pos, f, layout="other"),
+                 lambda: api.rope(q, None, pos, f, stream=side), lambda: api.rope(q, None, pos, torch.ones(33, device="cuda")),
+                 lambda: api.pages_append(p, pool, table, lens, k, k.bfloat16()),
+                 lambda: api.pages_append(p, pool[:-1], table, lens, k, k),
+                 lambda: api.pages_append(p, pool, table, lens[:1], k, k),
+                 lambda: api.pages_append(p, pool, table, lens, k, k.transpose(1, 2).contiguous().transpose(1, 2)),
+                 lambda: api.pages_append(p, pool, table, lens, k, k, n_new=4),
+                 lambda: api.pages_read(p, pool, table, lens), lambda: api.pages_read(p, pool, table, lens, k, out),
+                 lambda: api.tree_attn(p, pool, table, lens, q4, out, ws, k=k),
+                 lambda: api.tree_attn(p, pool, table, lens, q4, out[:, :2], ws),
+                 lambda: api.tree_attn(p, pool, table, lens, q4, out, ws[:1000]),
+                 lambda: api.tree_attn(p, pool, table, lens, q4, out, ws, k=k, v=k, mask=torch.ones(2, 3, device="cuda")),
+                 lambda: api.tree_attn(p, pool, table, lens, q4, out, ws, prefix_out=out)):
+        with pytest.raises(api.JoltError):
+            call()
+
+
 # ---- write and read back ---------------------------------------------------------------------------
 
 def coded(x, seed, b):

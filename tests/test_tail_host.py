@@ -130,7 +130,8 @@ def test_append_and_read_refusals():
 
     assert read(batch=0) == 0 and read(n=0) == 0
     for over in (dict(p=None), dict(pool=None), dict(table=None), dict(lens=None), dict(n=-1), dict(k=None, v=None),
-                 dict(v=FAKE + 4), dict(sb=12), dict(sh=-8), dict(mp=0)):
+                 dict(v=FAKE + 4), dict(sb=12), dict(sh=-8), dict(mp=0), dict(sh=248), dict(batch=2, sb=128),
+                 dict(batch=65536)):
         assert read(**over) == BAD, over
 
 
