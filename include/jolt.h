@@ -494,7 +494,7 @@ size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t 
  *   lse      device fp32 [batch][n_new][n_q], or NULL
  *   ws       device, >= jolt_tree_attn_workspace, 256-byte aligned, its first 4 bytes zero before the
  *            first call (the error word, read by jolt_check); calls sharing a ws must not overlap in time
- * Scores and softmax statistics are fp32. bf16 with more than 32 query rows (n_new * n_q / n_kv) runs its
+ * Scores and softmax statistics are fp32. bf16 with more than 16 query rows (n_new * n_q / n_kv) runs its
  * products on tcgen05, the rest on m16n8k16 MMAs. Asynchronous on `stream`. */
 jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
                            const int32_t* lens, int32_t batch, int32_t n_new, int32_t n_q, const int32_t* counts,

@@ -630,25 +630,28 @@ struct TreePlan {
 TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_pages) {
   TreePlan t{};
   const int rows = n_new * (n_q / p.n_kv);
-  if (rows > 32 && p.io_dtype == JOLT_BF16) {
+  // tcgen05 pays for 128 rows whatever their number, mma.sync for each 16: batch 16 of 8192 tokens, 8 KV heads:
+  // 16 rows 36.9 against 26.8 us, 32 rows 38.4 against 43.2, 64 rows 40 against 84; one sequence of 131072: 16
+  // rows 113.5 against 69.2 us, 32 rows 114.6 against 123.2; 32 rows over 512 tokens 18.8 against 22.2.
+  if (rows > 16 && p.io_dtype == JOLT_BF16) {
     t.tc = true;
     t.blocks = (rows + 127) / 128;
     t.least = 2;
     t.smem = tree_tc_smem(p.d_h);
   } else {
-  t.pack = rows <= 4;
-  t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  t.blocks = (rows + 8 * t.nt - 1) / (8 * t.nt);
-  t.least = kWarps;
-  t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
-  const int budget = (t.nt == 1 ? 100 : 190) * 1024;
-  t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
-  const int C = 8 * t.nt, qt = t.pack ? 1 : 2;
-  const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 4 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
-  const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
-  const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
-  const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
-  t.smem = std::max(head + std::max(ring, red), draft);
+    t.pack = rows <= 4;
+    t.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    t.blocks = (rows + 8 * t.nt - 1) / (8 * t.nt);
+    t.least = kWarps;
+    t.stage_bytes = kTile * (p.d_h * (p.b_k + p.b_v) / 8 + 8);
+    const int budget = (t.nt == 1 ? 100 : 190) * 1024;
+    t.stages = std::max(2, std::min(kMaxStages, budget / (kWarps * t.stage_bytes)));
+    const int C = 8 * t.nt, qt = t.pack ? 1 : 2;
+    const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 4 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
+    const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
+    const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
+    const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
+    t.smem = std::max(head + std::max(ring, red), draft);
   }
   // one block an SM for each 128 rows, or two where the registers allow: as many shares as are resident at once
   const int heads = p.n_kv * t.blocks, resident = 148 * (!t.tc && t.nt == 1 ? 2 : 1);
@@ -696,14 +699,17 @@ jolt_status launch_tree(const TreeArgs& a, const TreePlan& t, bool draft, cudaSt
 
 template <typename T, int D>
 jolt_status launch_tree_d(const TreeArgs& a, const TreePlan& t, bool draft, cudaStream_t st) {
-  if (t.tc) {
-    const jolt_status r = launch_tree_tc(a, D, draft, t.smem, st);
-    return r != JOLT_OK ? r : launch_merge<T, D, 128>(a, draft, st);
+  if constexpr (sizeof(T) == 2) {
+    if (t.tc) {
+      const jolt_status r = launch_tree_tc(a, D, draft, t.smem, st);
+      return r != JOLT_OK ? r : launch_merge<T, D, 128>(a, draft, st);
+    }
   }
   if (t.pack) return launch_tree<T, D, 1, true>(a, t, draft, st);
   if (t.nt == 1) return launch_tree<T, D, 1, false>(a, t, draft, st);
   if (t.nt == 2) return launch_tree<T, D, 2, false>(a, t, draft, st);
-  return launch_tree<T, D, 4, false>(a, t, draft, st);
+  if constexpr (sizeof(T) == 4) return launch_tree<T, D, 4, false>(a, t, draft, st);
+  return JOLT_ERR_INVALID_ARG;  // bf16 of more than 16 rows is t.tc
 }
 
 bool rows_ok(const void* x, int64_t s0, int64_t s1) {

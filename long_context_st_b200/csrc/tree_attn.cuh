@@ -472,7 +472,7 @@ __device__ __forceinline__ void draft_part(const TreeArgs& a, int b, int h, int 
 }
 #endif
 
-// The form for bf16 and more than 32 query rows a KV head (tree_tc.cu).
+// The form for bf16 and more than 16 query rows a KV head (tree_tc.cu).
 size_t tree_tc_smem(int d_h);
 // Place of feature f in a row of that form's code tiles (in elements) when its codes have 2^lnc a word:
 // quarter row m, piece i of it (pairs 4i .. 4i+3 of code_pair's order), at piece i * 4 + m.

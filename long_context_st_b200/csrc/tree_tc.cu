@@ -1,4 +1,4 @@
-// jolt_tree_attn for bf16 and more than 32 query rows a KV head: the products on tcgen05 (see tree_attn.cu
+// jolt_tree_attn for bf16 and more than 16 query rows a KV head: the products on tcgen05 (see tree_attn.cu
 // for the arithmetic, which is the same).
 //
 // A block takes 128 query rows (drafted token x head of the group) of one KV head and a range of the
@@ -133,7 +133,9 @@ __device__ __forceinline__ void ld_wait(uint32_t (&x)[16]) {
 // a 16-byte store phase then have one piece of eight rows, which the swizzle puts into eight slots.
 //
 // Keys: codes are whole numbers c 2^-24 already as the f16 bits of their fields (f16's subnormals, with a
-// field's place in its byte a further power of two that R q is divided by): one mask a pair.
+// field's place in its byte a further power of two that R q is divided by): one mask a pair. 2-bit keys are
+// widened to centred normal numbers, two operations a pair: as subnormals their products lose 8 of the sum's
+// 24 bits, which the fp32 log-sum-exp shows (3e-6).
 template <int D, int B>
 __device__ __forceinline__ void widen_keys(const uint32_t (&w)[4][D * B / 128], uint8_t* tile, const int (&off)[D / 32]) {
 #pragma unroll

@@ -470,6 +470,47 @@ def test_attention_rising_scores(cuda_ok, d, n, nq):
     check_case(c)
 
 
+# An MMA step adds 16 products and the sum so far, and drops from each what lies below 24 bits of the largest:
+# about sqrt(17 / 3) 2^-24 of it a step, taken as one-sided over the steps below; a row of 128 takes 8 steps, two
+# terms each: 16 * 2.4 * 2^-24 = 2^-18.7. Operands keep 22 bits, and the fp32 transforms' seven stages and the joins
+# of partial sums add some 2^-22: 2^-18 of the products' size in all, the largest product being counted with a
+# factor of two. Codes that entered as subnormals would lose 8 more bits at 2 bits, 6 at 4, 2 at 8.
+
+@pytest.mark.parametrize("io,b", [("f32", 2), ("f32", 4), ("f32", 8), ("bf16", 2)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 4, 12])
+def test_scores_keep_their_bits(cuda_ok, io, b, d, n):
+    """Sequences of one token: the log-sum-exp is the score itself."""
+    c = attn_case(61, [1] * 40, n, 4, 2, d, b, 4, 16, io, drafted=False)
+    p, pool, table, lens, q = c[:5]
+    _, lse = run_attn(c)
+    R = oracle.rotation_matrix(d, p.rot_seed)
+    qr = (f64(q) @ R.T) / math.sqrt(d)                                       # [B][n][4][d]
+    y = np.stack([s[0][:, 0] for s in stored_rows(p, pool, table, lens)])    # [B][2][d]
+    s = np.einsum("bnhgd,bhd->bnhg", qr.reshape(40, n, 2, 2, d), y).reshape(40, n, 4)
+    # the codes' part and the offsets' part are formed apart: both count
+    size = 2 * np.sqrt(np.mean(qr ** 2) * d) * (np.sqrt(np.mean(y ** 2)) + np.abs(y.mean(-1)).max())
+    assert np.sqrt(np.mean((f64(lse) - s) ** 2)) <= 2.0 ** -18 * size
+
+
+@pytest.mark.parametrize("b", [2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 4, 12])
+def test_outputs_keep_their_bits(cuda_ok, b, d, n):
+    """fp32 with q = 0: the output is the values' mean, each partial sum at most the rows' size."""
+    c = attn_case(62, [96, 40, 7], n, 4, 2, d, 4, b, 16, "f32", drafted=False)
+    p, pool, table, lens, q = c[:5]
+    q.zero_()
+    out, lse = run_attn(c)
+    R = oracle.rotation_matrix(d, p.rot_seed)
+    held = [s[1] for s in stored_rows(p, pool, table, lens)]
+    size = 2 * np.sqrt(np.mean(np.concatenate([v.reshape(-1) for v in held]) ** 2))
+    for i, v in enumerate(held):
+        want = np.repeat((v.mean(1) @ R), 2, axis=0)  # [4][d]
+        assert np.sqrt(np.mean((f64(out)[i] - want) ** 2)) <= 2.0 ** -18 * size
+        assert np.abs(f64(lse)[i] - math.log(lens[i])).max() <= 2.0 ** -21 * max(1.0, math.log(lens[i]))
+
+
 # ---- streams, graphs, devices ------------------------------------------------------------------------
 
 def test_captured_calls_follow_lengths_and_positions(cuda_ok):
