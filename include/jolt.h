@@ -413,19 +413,20 @@ jolt_status jolt_decode_attn_noalloc(const jolt_shape* shape, const jolt_cell_ch
  * bits as in the stored cache; pages start at multiples of jolt_pages_layout's page_bytes (a multiple
  * of 256). The pool must be 16-byte aligned.
  * Token t of sequence s is row t % page_size of page table[s*max_pages + t / page_size]
- * (table: device int32 [batch][max_pages]; entries past a sequence's tokens are not read).
+ * (table: device int32 [batch][max_pages], max_pages*page_size at most 2^24; entries past a sequence's
+ * tokens are not read).
  * lens: device int32 [batch], tokens each sequence holds; read when the kernels run, so a captured
  * graph follows them. Sequences may share the pages they read, not the pages they write.
  *
- * Device-side checks: a length outside [0, max_pages*page_size] is clamped, a table entry outside
- * [0, n_pages) makes its page's tokens invisible (reads, attention) or unwritten (append); both
- * set JOLT_ERR_INVALID_ARG in the error word. err (device int32, may be NULL) as in
+ * Device-side checks: a length outside [0, max_pages*page_size] is clamped (reads, attention) or leaves the
+ * sequence unwritten (append), a table entry outside [0, n_pages) makes its page's tokens invisible or
+ * unwritten; both set JOLT_ERR_INVALID_ARG in the error word. err (device int32, may be NULL) as in
  * jolt_quantize_pack: set, never cleared. batch is at most 65535; a call
  * with batch, n_new or n_out 0 returns JOLT_OK. */
 typedef struct {
   int32_t n_pages;      /* pages in the pool >= 1 */
   int32_t page_size;    /* tokens per page: 16, 32, 64 or 128 */
-  int32_t n_kv;         /* KV heads >= 1 */
+  int32_t n_kv;         /* KV heads, 1..4096 */
   int32_t d_h;          /* head dimension: 64 or 128 */
   int32_t b_k, b_v;     /* bits per key / value element: 2, 4 or 8 */
   int32_t io_dtype;     /* jolt_dtype of q, k, v and out */
@@ -480,7 +481,8 @@ size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t 
  * cache through jolt_decode_attn). With s_t = attn_scale * q.k_t over all visible tokens,
  * out = sum softmax(s)_t v_t and lse = log sum exp(s_t). A row that sees nothing gets out 0, lse -inf.
  *   q        device [batch][n_new][n_q][d_h] io dtype, heads contiguous, element strides q_stride_b and
- *            q_stride_t, multiples of 8; 16-byte aligned; n_q a multiple of n_kv, n_new <= 64
+ *            q_stride_t, multiples of 8; 16-byte aligned; n_q a multiple of n_kv, at most 4096 times
+ *            it; n_new <= 64
  *   k, v     device [batch][n_new][n_kv][d_h] io dtype, the drafted tokens' rows, strides kv_stride_b and
  *            kv_stride_t as in jolt_pages_append; both NULL: the drafted tokens see the pages and the
  *            prefix alone

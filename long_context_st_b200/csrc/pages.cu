@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
       const int h = int(r - bi * a.p.n_kv), i = int(bi - b * a.n_new);
       if (!a.counts || i < a.counts[b]) {
         const int from = a.src ? a.src[int64_t(b) * a.n_new + i] : i;
-        const int at = pages_len(a.p, b, a.err) + i;
-        if (from < 0 || from >= a.n_src || at >= (a.p.max_pages << a.p.ps_log2)) {
+        const int len = a.p.lens[b], at = len + i;
+        if (from < 0 || from >= a.n_src || len < 0 || len > (a.p.max_pages << a.p.ps_log2) - 1 - i) {
           report_error(a.err, JOLT_ERR_INVALID_ARG);
         } else {
           const int page = page_of(a.p, b, at, a.err);

@@ -670,7 +670,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
 
 bool tree_dims_ok(const jolt_pages* p, int batch, int n_new, int n_q, int max_pages) {
   return pages_ok(p) && batch >= 0 && batch <= 65535 && n_new >= 0 && n_new <= kMaxDraft && n_q >= p->n_kv &&
-         n_q % p->n_kv == 0 && n_q <= 65536 && max_pages >= 1 && int64_t(max_pages) * p->page_size <= (int64_t(1) << 24);
+         n_q % p->n_kv == 0 && n_q / p->n_kv <= 4096 && n_q <= 65536 && max_pages >= 1 && int64_t(max_pages) * p->page_size <= (int64_t(1) << 24);
 }
 
 template <typename T, int D, int TILE>

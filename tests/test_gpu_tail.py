@@ -214,6 +214,15 @@ def test_append_reports_bad_pages_sources_and_values(cuda_ok):
         codes, _ = page_rows(p, pool, 0)
         assert bool((codes[0, :, 14:] != 0x11).any(-1).all())  # tokens 14, 15 are written all the same
         assert bool((codes[1:] == 0x11).all()) and bool((codes[0, :, :14] == 0x11).all())
+    for length in (-1, 29, 33):  # 29: the last of four rows is past the table; -1 and 33: no length at all
+        pool, err = api.new_pool(p), i32([0])
+        pool.fill_(0x11)
+        api.pages_append(p, pool, i32([[0, 1]]), i32([length]), k, k, err=err)
+        codes, _ = page_rows(p, pool, 0)
+        want = torch.zeros_like(codes, dtype=torch.bool).any(-1)
+        if length == 29:
+            want[1, :, 13:] = True
+        assert int(err) == -1 and torch.equal((codes != 0x11).any(-1), want)
     for bad in (float("nan"), float("inf"), 3e38):
         x = k.clone()
         x[0, 2, 1, 5] = bad

@@ -149,7 +149,7 @@ def test_attention_refusals():
                  dict(lens=None), dict(batch=-1), dict(n=65), dict(n=-1), dict(nq=7), dict(nq=0), dict(q=None), dict(q=FAKE + 2),
                  dict(qb=4), dict(qt=1023), dict(k=None), dict(v=None), dict(kt=3), dict(scale=0.0), dict(scale=-1.0),
                  dict(scale=math.nan), dict(scale=math.inf), dict(po=FAKE), dict(pl=FAKE), dict(out=None), dict(out=FAKE + 8),
-                 dict(ws=None), dict(ws=FAKE + 16)):
+                 dict(ws=None), dict(ws=FAKE + 16), dict(nq=2 * 4097)):
         assert call(**over) == BAD, over
     need = _lib.lib().jolt_tree_attn_workspace(C.byref(p), 1, 2, 8, 4)
     assert need > 256 and call(wsb=need - 1) == -6
