@@ -64,11 +64,14 @@ __device__ __forceinline__ int64_t out_row(const TreeArgs& a, int b, int h, int 
 // A (KV head, row block) has `shares` blocks for the tiles of all sequences. Balanced: a split has c tiles, the
 // least c (of a few) for which all sequences' splits number at most `shares`, so a ragged batch keeps every
 // block equally long (lengths 64K, 56K, 48K, 40K: 23% over a division of each sequence by the same number).
-// The lengths are on the device, so every warp works this out for itself; lane i has sequences 4 i .. + 3.
+// The lengths are on the device, so a warp works this out for itself; lane i has sequences 4 i .. + 3.
 constexpr int kMaxBalanced = 128;  // sequences
 struct Shares {
   int tiles[4], c;
 };
+// ceil(t / c) for t + c <= 2^21, rc = fl(1 / c): (t + c - 1/2) / c is 1 / (2 c) or more from a whole number, 2^-22 of
+// itself, and the two roundings come to 2^-23.
+__device__ __forceinline__ int ceil_div(int t, int c, float rc) { return int((float(t + c - 1) + 0.5f) * rc); }
 template <int TILE>
 __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int lane) {
   Shares s;
@@ -92,8 +95,9 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int lane) {
     const int left = max(a.shares - min(k, a.batch), 1);
     s.c = max(least, (sum + left - 1) / left);
     int n = 0;
+    const float rc = __frcp_rn(float(s.c));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += (s.tiles[i] + s.c - 1) / s.c;
+    for (int i = 0; i < 4; ++i) n += ceil_div(s.tiles[i], s.c, rc);
     if (k >= a.batch || int(__reduce_add_sync(0xffffffffu, n)) <= a.shares) return s;
   }
 }
@@ -119,8 +123,9 @@ __device__ __forceinline__ bool work_of(const TreeArgs& a, Work* w) {
   if (a.balanced) {
     const Shares s = shares_of<TILE>(a, lane);
     int n[4], mine = 0;
+    const float rc = __frcp_rn(float(s.c));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine += n[i] = (s.tiles[i] + s.c - 1) / s.c;
+    for (int i = 0; i < 4; ++i) mine += n[i] = ceil_div(s.tiles[i], s.c, rc);
     int first = mine;  // splits before this lane's sequences
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {

@@ -61,9 +61,11 @@ struct Smem {
   static constexpr int l = ref + 512;              // [128] the odd tiles' sums
   static constexpr int vis = l + 512;              // [4][4] words: visible tokens
   static constexpr int ve = vis + 64;              // [4][2] value exponent of this tile and of the one before
-  static constexpr int bars = ve + 32;             // 22 mbarriers
-  static constexpr int slot = bars + 176;          // tensor memory base
-  static constexpr int used = slot + 16;
+  static constexpr int bars = ve + 32;             // 23 mbarriers
+  static constexpr int slot = bars + 192;          // tensor memory base
+  static constexpr int work = slot + 16;           // Work, rows
+  static constexpr int un = work + 48;             // power of two of the scores' accumulators
+  static constexpr int used = un + 16;
   static constexpr int total = used + 1024;        // swizzled tiles start at 1024-byte boundaries
 };
 
@@ -200,7 +202,6 @@ struct Ctx {
   uint8_t* smem;
   uint32_t sb, bar0;
   int n_tiles, tile0, len, h, b;
-  float unscale;  // of the scores' accumulators
   // by tile, four of each (of v_full two): the next use of a barrier can't complete before everyone who waits
   // for this one has seen it
   __device__ __forceinline__ uint32_t k_full(int n) const { return bar0 + 8 * (n & 3); }
@@ -209,7 +210,10 @@ struct Ctx {
   __device__ __forceinline__ uint32_t v_full(int n) const { return bar0 + 96 + 8 * (n & 1); }
   __device__ __forceinline__ uint32_t pv_done(int n) const { return bar0 + 112 + 8 * (n & 3); }
   __device__ __forceinline__ uint32_t sc_full(int n) const { return bar0 + 144 + 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t q_done() const { return bar0 + 176; }
 };
+// Softmax, values, MMA and scales warps: R q is there, and the staging of its product is free.
+__device__ __forceinline__ void q_sync() { asm volatile("bar.sync 4, 704;" ::: "memory"); }
 
 // The pages of the two 16-token halves of a warp's 32 tokens. Table entries are read a tile before they are
 // needed. A half past the end, or without a page (which is reported), is read from page 0 and not seen.
@@ -296,6 +300,8 @@ __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
   };
   entry(0);
   fetch(0);
+  q_sync();
+  const float unscale = *reinterpret_cast<const float*>(c.smem + S::un);
   int ve = -30;
   for (int n = 0; n < c.n_tiles; ++n) {
     const int q = n & 3;
@@ -307,7 +313,7 @@ __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
     for (int i = 0; i < 4; ++i) {
       const float2 k = h2_floats(ku[i]), v = h2_floats(vu[i]);
       const bool here = (seen >> i) & 1;
-      sc[i] = here ? k.x * c.unscale : 0.f;
+      sc[i] = here ? k.x * unscale : 0.f;
       ze[i] = here ? k.y + ko * k.x : 0.f;
       if (here) most = fmaxf(most, fmaxf(fabsf(v.y), fabsf(v.y + vtop * v.x)));
     }
@@ -360,6 +366,7 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   };
   hv.read(a, c, c.tile0 * kTok + wq * 32);
   fetch(0);
+  q_sync();
   for (int n = 0; n < c.n_tiles; ++n) {
     const int s = n & 1;
     if (!wait_all(c.sc_full(n), (n >> 2) & 1, a.err)) return;  // ve of this tile
@@ -645,33 +652,143 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
   }
 }
 
+// Feature at place p of a code tile's row (place_of's inverse).
+template <int D>
+__device__ __forceinline__ int feature_at(int p, int lnc) {
+  const int half = 1 << (lnc - 1), pair = (p >> 5) * 4 + ((p & 7) >> 1);
+  return ((p >> 3) & 3) * (D / 4) + ((pair >> (lnc - 1)) << lnc) + (pair & (half - 1)) + ((p & 1) << (lnc - 1));
+}
+
+// Warps 0-15 with warp 24: R q of the block's rows as two f16 terms in the tiles' order, times one power of two for
+// all rows: the largest element then has 2^14, and the second term's last place is 2^-24, 2^-39 of it. The
+// transform is itself a product on tcgen05: q, bf16 as given, with the matrix of its signs (row: a place's feature),
+// both staged where the values' tiles will be, so that no row waits for shuffles (7400 cycles by a transform in
+// registers, of 28000 for a block of one tile).
+template <int D>
+__device__ void q_stage(const TreeArgs& a, const Ctx<D>& c, int tid, int r0, int rows) {
+  using S = Smem<D>;
+  constexpr int V = D / 8, kQ = 128 * V / 512, kB = D * V / 512;  // 16-byte pieces of a row; of a thread
+  const int lane = tid & 31, t = tid % V, row0 = tid / V;
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(c.b) * a.qsb + int64_t(c.h) * a.gq * D;
+  uint4 x[kQ];
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int r = row0 + i * (512 / V);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) x[i] = *reinterpret_cast<const uint4*>(qb + q_offset(a, r0 + r, D) + t * 8);
+  }
+  uint32_t neg = 0, first = 0;  // this piece's eight signs; those of the first 32 features
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+    const uint32_t bits = __ballot_sync(0xffffffffu, rot_sign(a.p.seed, 32 * w + lane) < 0.f);
+    if (w == 0) first = bits;
+    if ((t >> 2) == w) neg = (bits >> (8 * (t & 3))) & 0xFFu;
+  }
+  uint8_t* const signs = c.smem + S::v;
+#pragma unroll
+  for (int i = 0; i < kB; ++i) {
+    const int p = row0 + i * (512 / V), f = feature_at<D>(p, log2_codes(a.p.bk));
+    // bit e: element (f, 8 t + e) is negative, the parity of f & (8 t + e) and the column's own sign
+    uint32_t bits = neg ^ ((f & 1) ? 0xAAu : 0u) ^ ((f & 2) ? 0xCCu : 0u) ^ ((f & 4) ? 0xF0u : 0u);
+    if (__popc(f & (8 * t)) & 1) bits ^= 0xFFu;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = 0x3F803F80u | ((bits << (15 - 2 * e)) & 0x8000u) | ((bits << (30 - 2 * e)) & 0x80000000u);
+    *reinterpret_cast<uint4*>(signs + (t >> 3) * S::kChunk + p * 128 + (((t & 7) ^ (p & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int r = row0 + i * (512 / V);
+    *reinterpret_cast<uint4*>(signs + S::kTile + (t >> 3) * S::kChunk + r * 128 + (((t & 7) ^ (r & 7)) << 4)) = x[i];
+    // the elements of H x add up to D x_0
+    if (t == 0)
+      reinterpret_cast<float*>(c.smem + S::qs)[r] =
+          __uint_as_float(x[i].x << 16) * ((first & 1) ? -a.scale2 : a.scale2) * (float(D) * rsqrtf(float(D)));
+  }
+  fence_proxy_async_smem();
+  asm volatile("bar.sync 3, 544;" ::: "memory");
+}
+template <int D>
+__device__ void q_finish(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, int warp, int lane) {
+  using S = Smem<D>;
+  constexpr int C = D / 4;  // a thread has a row's quarter
+  const int quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
+  wait_all(c.q_done(), 0, a.err);  // a wait that gave up is reported, and ends the call like any other
+  tc_fence_after();
+  uint32_t x[C];
+  if constexpr (C == 32) tmem_ld32(tmem + (uint32_t(quarter * 32) << 16) + part * C, x);
+  else tmem_ld16(tmem + (uint32_t(quarter * 32) << 16) + part * C, x);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < C; ++i) asm volatile("" : "+r"(x[i]));  // not read before the wait
+  const float f = a.scale2 * rsqrtf(float(D));
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) top = fmaxf(top, fabsf(__uint_as_float(x[i]) * f));
+  if (!(top < INFINITY)) top = 0.f;  // a row that is not finite is on its own
+  top = warp_max(top);
+  float* rs = reinterpret_cast<float*>(c.smem + S::rs);
+  if (lane == 0) rs[warp] = top;
+  asm volatile("bar.sync 2, 512;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, rs[i]);
+  int k = 0;
+  if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
+  if (warp + lane == 0) *reinterpret_cast<float*>(c.smem + S::un) = pow2i((a.p.bk == 2 ? 0 : 24) - k);
+  // less a 4-bit field's place in its byte, that of odd pairs (b times a pair's number is 0 modulo 8 at 8 bits; 2-bit
+  // codes are normal numbers)
+  const float up = pow2i(k), odd = a.p.bk == 4 ? 0.0625f : 1.f;
+  uint8_t* const q = c.smem + S::q + r * 128;
+#pragma unroll
+  for (int i = 0; i < C / 8; ++i) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float y0 = __uint_as_float(x[8 * i + 2 * e]) * f * up * ((e & 1) ? odd : 1.f);
+      const float y1 = __uint_as_float(x[8 * i + 2 * e + 1]) * f * up * ((e & 1) ? odd : 1.f);
+      h[e] = h2_pack(y0, y1);
+      const float2 z = h2_floats(h[e]);
+      l[e] = h2_pack(y0 - z.x, y1 - z.y);
+    }
+    const int piece = part * (C / 8) + i;
+    uint8_t* dst = q + (piece >> 3) * S::kChunk + (((piece & 7) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + S::kTile) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  q_sync();
+  tc_fence_after();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
   using S = Smem<D>;
-  constexpr int E = D / 32;
   extern __shared__ uint8_t raw[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Work wk;
-  if (!work_of<kTok>(a, &wk)) return;
-  const int h = wk.h, r0 = wk.block * kRows, b = wk.b, split = wk.split;
   uint8_t* smem = align_smem_1024(raw);
-  if (split == a.splits) {
-    draft_part<__nv_bfloat16, D, kRows, kThreads>(a, b, h, r0, smem);
+  Work wk;
+  if (int(blockIdx.x) >= a.shares * a.p.n_kv * a.blocks) {
+    work_of<kTok>(a, &wk);
+    draft_part<__nv_bfloat16, D, kRows, kThreads>(a, wk.b, wk.h, wk.block * kRows, smem);
     return;
   }
-  const int rows = min(kRows, draft_count(a, b) * a.gq - r0);
-  if (rows <= 0) return;
   Ctx<D> c;
   c.smem = smem;
   c.sb = smem_u32(smem);
   c.bar0 = c.sb + S::bars;
-  c.h = h;
-  c.b = b;
-  c.len = wk.len;
-  c.tile0 = wk.tile0;
-  c.n_tiles = wk.n_tiles;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::slot);
+  Work* shared_work = reinterpret_cast<Work*>(smem + S::work);
+  int* shared_rows = reinterpret_cast<int*>(shared_work + 1);
+  if (warp == 0) {  // one warp: all 26 at once would take 5000 cycles
+    const bool any = work_of<kTok>(a, &wk);
+    const int rows = any ? min(kRows, draft_count(a, wk.b) * a.gq - wk.block * kRows) : 0;
+    if (lane == 0) {
+      *shared_work = wk;
+      *shared_rows = rows;
+    }
+  }
   if (warp == 24) {
     tmem_alloc(smem_u32(slot), 512);
     if (lane == 0) {
@@ -683,104 +800,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
         mbar_init(c.pv_done(n), 1);
         mbar_init(c.sc_full(n), 1);
       }
+      mbar_init(c.q_done(), 1);
       fence_mbar_init();
     }
     __syncwarp();
   }
-  // R q as two f16 terms, scaled by one power of two for all rows: the largest element then has 2^14, and the
-  // second term's last place is 2^-24, 2^-39 of it
-  {
-    const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
-    const float isd = rsqrtf(float(D));
-    constexpr int kW = kThreads / 32, kPer = (kRows + kW - 1) / kW;
-    float v[kPer][E], top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = warp + i * kW;
-      uint32_t w[E / 2];
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) w[e] = 0;
-      if (r < rows) load_words<E / 2>(reinterpret_cast<const uint8_t*>(qb + q_offset(a, r0 + r, D) + lane * E), w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-    }
-    for (int i = threadIdx.x; i < (kRows - rows) * (D / 8) * 2; i += kThreads) {
-      const int r = rows + i / (D / 4), at16 = i % (D / 4);  // 16-byte places of a row, both terms (any order)
-      *reinterpret_cast<uint4*>(smem + S::q + (at16 >> 3) * S::kChunk + r * 128 + (at16 & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
-    for (int r = rows + threadIdx.x; r < kRows; r += kThreads) reinterpret_cast<float*>(smem + S::qs)[r] = 0.f;
-    int at[E];
-    float sign[E], low[E];  // low: 2^-(a code field's place in its byte)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      at[e] = place_of(lane * E + e, log2_codes(a.p.bk), D);
-      sign[e] = rot_sign(a.p.seed, lane * E + e) * a.scale2;
-      low[e] = a.p.bk == 2 ? 1.f : pow2i(-(a.p.bk * ((at[e] & 7) >> 1) & 7));  // b (pair % (8 / b)) = (b pair) % 8
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = warp + i * kW;
-      if (r >= rows) break;  // rows past the last are zeros
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] *= sign[e];
-      // the elements of H x add up to D x_0
-      if (lane == 0) reinterpret_cast<float*>(smem + S::qs)[r] = v[i][0] * (float(D) * isd);
-      warp_fwht<E>(v[i]);
-      float most = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        v[i][e] *= isd;
-        most = fmaxf(most, fabsf(v[i][e]));
-      }
-      if (most < INFINITY) top = fmaxf(top, most);  // a row that is not finite is on its own
-    }
-    top = warp_max(top);
-    if (lane == 0) reinterpret_cast<float*>(smem + S::rs)[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kW; ++i) top = fmaxf(top, reinterpret_cast<const float*>(smem + S::rs)[i]);
-    int k = 0;
-    if (top > 0.f) k = min(max(14 - (int(__float_as_uint(top) >> 23) - 127), -100), 100);
-    c.unscale = pow2i((a.p.bk == 2 ? 0 : 24) - k);
-    const float up = pow2i(k);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = warp + i * kW;
-      if (r >= rows) break;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float x = v[i][e] * up * low[e];
-        const __half x1 = __float2half_rn(x), x2 = __float2half_rn(x - __half2float(x1));
-        const int off = (at[e] >> 6) * S::kChunk + r * 128 + ((((at[e] >> 3) & 7) ^ (r & 7)) << 4) + (at[e] & 7) * 2;
-        *reinterpret_cast<__half*>(smem + S::q + off) = x1;
-        *reinterpret_cast<__half*>(smem + S::q + S::kTile + off) = x2;
-      }
-    }
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  const int rows = *shared_rows;
+  if (rows <= 0) {
+    if (warp == 24) tmem_dealloc(tmem, 512);
+    return;
+  }
+  wk = *shared_work;
+  const int r0 = wk.block * kRows;
+  c.h = wk.h;
+  c.b = wk.b;
+  c.len = wk.len;
+  c.tile0 = wk.tile0;
+  c.n_tiles = wk.n_tiles;
   if (warp < 16) {
+    q_stage<D>(a, c, tid, r0, rows);
+    q_finish<D>(a, c, tmem, warp, lane);
     // a warp reaches the 32 lanes of its quarter, warp % 4
-    softmax_role<D>(a, c, tmem, warp >> 3, (warp & 3) * 32 + ((warp >> 2) & 1) * 16, lane, r0, rows, split);
-  } else if (warp < 24) {
+    softmax_role<D>(a, c, tmem, warp >> 3, (warp & 3) * 32 + ((warp >> 2) & 1) * 16, lane, r0, rows, wk.split);
+  } else if (warp < 20) {
     if (c.n_tiles > 0) {
-      const int bits = warp < 20 ? a.p.bk : a.p.bv;
-      if (warp < 20) {
-        if (bits == 4) keys_role<D, 4>(a, c, warp & 3, lane);
-        else if (bits == 8) keys_role<D, 8>(a, c, warp & 3, lane);
-        else keys_role<D, 2>(a, c, warp & 3, lane);
-      } else {
-        if (bits == 4) values_role<D, 4>(a, c, warp & 3, lane);
-        else if (bits == 8) values_role<D, 8>(a, c, warp & 3, lane);
-        else values_role<D, 2>(a, c, warp & 3, lane);
-      }
+      if (a.p.bk == 4) keys_role<D, 4>(a, c, warp & 3, lane);
+      else if (a.p.bk == 8) keys_role<D, 8>(a, c, warp & 3, lane);
+      else keys_role<D, 2>(a, c, warp & 3, lane);
     }
+  } else if (warp == 24) {
+    asm volatile("bar.sync 3, 544;" ::: "memory");
+    tc_fence_after();
+    if (lane == 0) {
+      const uint64_t qd = smem_desc_sw128(c.sb + S::v + S::kTile, 16, 1024), sd = smem_desc_sw128(c.sb + S::v, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * S::kChunk + (kk & 3) * 32) >> 4;
+        mma_bf16(tmem, qd + at, sd + at, idesc_bf16_f32(kRows, D, 0, 0), kk > 0);
+      }
+      mma_commit(c.q_done());
+    }
+    __syncwarp();
+    q_sync();
+    tc_fence_after();
+    mma_role<D>(a, c, tmem, lane);
+  } else if (c.n_tiles == 0) {
+    q_sync();
+  } else if (warp == 25) {
+    scales_role<D>(a, c, lane);
   } else {
-    if (warp == 24) mma_role<D>(a, c, tmem, lane);
-    if (warp == 25 && c.n_tiles > 0) scales_role<D>(a, c, lane);
+    if (a.p.bv == 4) values_role<D, 4>(a, c, warp & 3, lane);
+    else if (a.p.bv == 8) values_role<D, 8>(a, c, warp & 3, lane);
+    else values_role<D, 2>(a, c, warp & 3, lane);
   }
   tc_fence_before();
   __syncthreads();
