@@ -88,12 +88,14 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs& a, int lane) {
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
   top = __reduce_max_sync(0xffffffffu, top);
-  const int least = max(a.least, (top + a.splits - 1) / a.splits);
+  const int least = max(a.least, ceil_div(top, a.splits, __frcp_rn(float(a.splits))));
   // c = sum / (shares - k) does for some k <= batch: each sequence rounds up by less than one
   const int step = max(1, a.batch >> 3);
   for (int k = 0;; k += step) {
     const int left = max(a.shares - min(k, a.batch), 1);
-    s.c = max(least, (sum + left - 1) / left);
+    // sums that ceil_div does not take exactly: a little more than sum / left
+    const float rl = __frcp_rn(float(left));
+    s.c = max(least, sum < (1 << 20) ? ceil_div(sum, left, rl) : int(float(sum) * rl * 1.000001f) + 1);
     int n = 0;
     const float rc = __frcp_rn(float(s.c));
 #pragma unroll

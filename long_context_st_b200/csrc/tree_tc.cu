@@ -661,30 +661,20 @@ __device__ __forceinline__ int feature_at(int p, int lnc) {
 
 // Warps 0-15 with warp 24: R q of the block's rows as two f16 terms in the tiles' order, times one power of two for
 // all rows: the largest element then has 2^14, and the second term's last place is 2^-24, 2^-39 of it. The
-// transform is itself a product on tcgen05: q, bf16 as given, with the matrix of its signs (row: a place's feature),
-// both staged where the values' tiles will be, so that no row waits for shuffles (7400 cycles by a transform in
-// registers, of 28000 for a block of one tile).
+// transform is itself a product on tcgen05: q, bf16 as given, with the matrix of its signs (row: a place's feature;
+// warps 8-23 form it while warp 0 finds the block's work), both staged where the values' tiles will be, so that
+// no row waits for shuffles (7400 cycles by a transform in registers, of 28000 for a block of one tile).
 template <int D>
-__device__ void q_stage(const TreeArgs& a, const Ctx<D>& c, int tid, int r0, int rows) {
+__device__ void q_signs(const TreeArgs& a, uint8_t* signs, int tid) {
   using S = Smem<D>;
-  constexpr int V = D / 8, kQ = 128 * V / 512, kB = D * V / 512;  // 16-byte pieces of a row; of a thread
+  constexpr int V = D / 8, kB = D * V / 512;  // 16-byte pieces of a row; of a thread
   const int lane = tid & 31, t = tid % V, row0 = tid / V;
-  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(c.b) * a.qsb + int64_t(c.h) * a.gq * D;
-  uint4 x[kQ];
-#pragma unroll
-  for (int i = 0; i < kQ; ++i) {
-    const int r = row0 + i * (512 / V);
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows) x[i] = *reinterpret_cast<const uint4*>(qb + q_offset(a, r0 + r, D) + t * 8);
-  }
-  uint32_t neg = 0, first = 0;  // this piece's eight signs; those of the first 32 features
+  uint32_t neg = 0;  // this piece's eight signs
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {
     const uint32_t bits = __ballot_sync(0xffffffffu, rot_sign(a.p.seed, 32 * w + lane) < 0.f);
-    if (w == 0) first = bits;
     if ((t >> 2) == w) neg = (bits >> (8 * (t & 3))) & 0xFFu;
   }
-  uint8_t* const signs = c.smem + S::v;
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
     const int p = row0 + i * (512 / V), f = feature_at<D>(p, log2_codes(a.p.bk));
@@ -696,14 +686,27 @@ __device__ void q_stage(const TreeArgs& a, const Ctx<D>& c, int tid, int r0, int
     for (int e = 0; e < 4; ++e) w[e] = 0x3F803F80u | ((bits << (15 - 2 * e)) & 0x8000u) | ((bits << (30 - 2 * e)) & 0x80000000u);
     *reinterpret_cast<uint4*>(signs + (t >> 3) * S::kChunk + p * 128 + (((t & 7) ^ (p & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+template <int D>
+__device__ void q_stage(const TreeArgs& a, const Ctx<D>& c, int tid, int r0, int rows) {
+  using S = Smem<D>;
+  constexpr int V = D / 8, kQ = 128 * V / 512;  // 16-byte pieces of a row; of a thread
+  const int t = tid % V, row0 = tid / V;
+  const float qs = rot_sign(a.p.seed, 0) * a.scale2 * (float(D) * rsqrtf(float(D)));
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + int64_t(c.b) * a.qsb + int64_t(c.h) * a.gq * D;
+  uint4 x[kQ];
 #pragma unroll
   for (int i = 0; i < kQ; ++i) {
     const int r = row0 + i * (512 / V);
-    *reinterpret_cast<uint4*>(signs + S::kTile + (t >> 3) * S::kChunk + r * 128 + (((t & 7) ^ (r & 7)) << 4)) = x[i];
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) x[i] = *reinterpret_cast<const uint4*>(qb + q_offset(a, r0 + r, D) + t * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) {
+    const int r = row0 + i * (512 / V);
+    *reinterpret_cast<uint4*>(c.smem + S::v + S::kTile + (t >> 3) * S::kChunk + r * 128 + (((t & 7) ^ (r & 7)) << 4)) = x[i];
     // the elements of H x add up to D x_0
-    if (t == 0)
-      reinterpret_cast<float*>(c.smem + S::qs)[r] =
-          __uint_as_float(x[i].x << 16) * ((first & 1) ? -a.scale2 : a.scale2) * (float(D) * rsqrtf(float(D)));
+    if (t == 0) reinterpret_cast<float*>(c.smem + S::qs)[r] = __uint_as_float(x[i].x << 16) * qs;
   }
   fence_proxy_async_smem();
   asm volatile("bar.sync 3, 544;" ::: "memory");
@@ -788,6 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const TreeArgs a) {
       *shared_work = wk;
       *shared_rows = rows;
     }
+  }
+  if (warp >= 8 && warp < 24) {
+    q_signs<D>(a, smem + S::v, tid - 256);
+    fence_proxy_async_smem();
   }
   if (warp == 24) {
     tmem_alloc(smem_u32(slot), 512);
