@@ -144,37 +144,32 @@ __device__ __forceinline__ void ld_wait(uint32_t (&x)[16]) {
 // widened to centred normal numbers, two operations a pair: as subnormals their products lose 8 of the sum's
 // 24 bits, which the fp32 log-sum-exp shows (3e-6).
 template <int D, int B>
-__device__ __forceinline__ void widen_keys(const uint32_t (&w)[4][D * B / 128], uint8_t* tile, const int (&off)[D / 32]) {
+__device__ __forceinline__ void widen_keys(const uint32_t (&w)[D * B / 128], uint8_t* tile, const int (&off)[D / 32]) {
 #pragma unroll
-  for (int it = 0; it < 4; ++it)
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t h[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        h[x] = B == 2 ? code_pair<B, D * B / 128>(w[it], 4 * i + x) : field_pair<B, D * B / 128>(w[it], 4 * i + x);
-      *reinterpret_cast<uint4*>(tile + off[i] + it * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    for (int x = 0; x < 4; ++x)
+      h[x] = B == 2 ? code_pair<B, D * B / 128>(w, 4 * i + x) : field_pair<B, D * B / 128>(w, 4 * i + x);
+    *reinterpret_cast<uint4*>(tile + off[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
 }
 // Values: dequantised, code * scale + zero in f16 by one fused multiply-add from the field's bits, in units of
 // 2^(ve - kVExp): scale[F] holds scale * 2^(24 - place) for the F places of a field in its byte.
 template <int D, int B>
-__device__ __forceinline__ void widen_values(const uint32_t (&w)[4][D * B / 128], const float2 (&sz)[4], uint8_t* tile,
+__device__ __forceinline__ void widen_values(const uint32_t (&w)[D * B / 128], float2 sz, uint8_t* tile,
                                              const int (&off)[D / 32]) {
+  constexpr int F = 8 / B;
+  uint32_t s[F];
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    constexpr int F = 8 / B;
-    uint32_t s[F];
+  for (int f = 0; f < F; ++f) s[f] = h2_pack(sz.x * pow2i(-B * f), sz.x * pow2i(-B * f));
+  const uint32_t z = h2_pack(sz.y, sz.y);
 #pragma unroll
-    for (int f = 0; f < F; ++f) s[f] = h2_pack(sz[it].x * pow2i(-B * f), sz[it].x * pow2i(-B * f));
-    const uint32_t z = h2_pack(sz[it].y, sz[it].y);
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t h[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) h[x] = h2_fma(field_pair<B, D * B / 128>(w[it], 4 * i + x), s[(4 * i + x) % F], z);
-      *reinterpret_cast<uint4*>(tile + off[i] + it * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    for (int x = 0; x < 4; ++x) h[x] = h2_fma(field_pair<B, D * B / 128>(w, 4 * i + x), s[(4 * i + x) % F], z);
+    *reinterpret_cast<uint4*>(tile + off[i]) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 // Where the lane's pieces of its row group go; row groups are 1024 bytes apart.
@@ -187,14 +182,12 @@ __device__ __forceinline__ void piece_offsets(int row0, int g, int m, int (&off)
   }
 }
 
-// Raw codes of this warp's 32 token rows: two 16-token halves at p0 and p1.
+// Raw codes of rows it * 8 + g of this warp's 32 token rows: two 16-token halves at p[0] and p[1]. A group's next
+// codes are asked for as soon as it is widened: waiting for a whole tile's at once took half of these warps' time.
 template <int D, int B>
-__device__ __forceinline__ void load_raw(const uint8_t* p0, const uint8_t* p1, uint32_t (&w)[4][D * B / 128]) {
-  constexpr int W = D * B / 128, RB = D * B / 8;
-  load_words<W>(p0, w[0]);
-  load_words<W>(p0 + 8 * RB, w[1]);
-  load_words<W>(p1, w[2]);
-  load_words<W>(p1 + 8 * RB, w[3]);
+__device__ __forceinline__ void load_raw(const uint8_t* const (&p)[2], uint32_t at0, uint32_t at1, int it,
+                                         uint32_t (&w)[D * B / 128]) {
+  load_words<D * B / 128>((it < 2 ? p[0] + at0 : p[1] + at1) + (it & 1) * 8 * (D * B / 8), w);
 }
 
 template <int D>
@@ -254,22 +247,28 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   const uint32_t at0 = a.p.kc + (uint32_t(c.h) * ps + ((wq * 32) & (ps - 1)) + g) * uint32_t(D * BK / 8) + m * (D * BK / 32);
   const uint32_t at1 = at0 + (ps == 16 ? 0 : 16 * (D * BK / 8));
   Halves<D> hv;
-  auto fetch = [&](int n) {
+  const uint8_t* page[2];
+  auto pages = [&](int n) {
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    const uint8_t* page[2];
     hv.pages(a, c, tok0, page);
     hv.read(a, c, tok0 + kTok);
-    load_raw<D, BK>(page[0] + at0, page[1] + at1, w);
   };
   hv.read(a, c, c.tile0 * kTok + wq * 32);
-  fetch(0);
+  pages(0);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) load_raw<D, BK>(page, at0, at1, it, w[it]);
   for (int n = 0; n < c.n_tiles; ++n) {
+    const bool more = n + 1 < c.n_tiles;
+    if (more) pages(n + 1);
     if (n >= 2 && !wait_all(c.s_done(n - 2), ((n - 2) >> 2) & 1, a.err)) return;
-    widen_keys<D, BK>(w, c.smem + S::k + (n & 1) * S::kTile, off);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      widen_keys<D, BK>(w[it], c.smem + S::k + (n & 1) * S::kTile + it * 1024, off);
+      if (more) load_raw<D, BK>(page, at0, at1, it, w[it]);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.k_full(n));
-    if (n + 1 < c.n_tiles) fetch(n + 1);
   }
 }
 
@@ -351,21 +350,23 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   const uint32_t sz0 = a.p.vs + (head + in_page) * 4, sz1 = sz0 + (ps == 16 ? 0 : 64);
   Halves<D> hv;
   int seen;  // bit it: the lane's row of group it
-  auto fetch = [&](int n) {
+  const uint8_t* page[2];
+  auto pages = [&](int n) {
     const int tok0 = (c.tile0 + n) * kTok + wq * 32;
-    const uint8_t* page[2];
     const int there = hv.pages(a, c, tok0, page);
     hv.read(a, c, tok0 + kTok);
     seen = 0;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      seen |= int(((there >> (it >> 1)) & 1) && tok0 + it * 8 + g < c.len) << it;
-      raw[it] = *reinterpret_cast<const __half2*>(page[it >> 1] + (it < 2 ? sz0 : sz1) + (it & 1) * 32);
-    }
-    load_raw<D, BV>(page[0] + at0, page[1] + at1, w);
+    for (int it = 0; it < 4; ++it) seen |= int(((there >> (it >> 1)) & 1) && tok0 + it * 8 + g < c.len) << it;
+  };
+  auto load = [&](int it) {
+    raw[it] = *reinterpret_cast<const __half2*>(page[it >> 1] + (it < 2 ? sz0 : sz1) + (it & 1) * 32);
+    load_raw<D, BV>(page, at0, at1, it, w[it]);
   };
   hv.read(a, c, c.tile0 * kTok + wq * 32);
-  fetch(0);
+  pages(0);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) load(it);
   q_sync();
   for (int n = 0; n < c.n_tiles; ++n) {
     const int s = n & 1;
@@ -377,12 +378,17 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
       const float2 f = __half22float2(raw[it]);
       sz[it] = (seen >> it) & 1 ? make_float2(f.x * (down * 16777216.f), f.y * down) : make_float2(0.f, 0.f);
     }
+    const bool more = n + 1 < c.n_tiles;
+    if (more) pages(n + 1);
     if (n >= 2 && !wait_all(c.pv_done(n - 2), ((n - 2) >> 2) & 1, a.err)) return;
-    widen_values<D, BV>(w, sz, c.smem + S::v + s * S::kTile, off);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      widen_values<D, BV>(w[it], sz[it], c.smem + S::v + s * S::kTile + it * 1024, off);
+      if (more) load(it);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(c.v_full(n));
-    if (n + 1 < c.n_tiles) fetch(n + 1);
   }
 }
 
