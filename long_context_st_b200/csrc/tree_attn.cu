@@ -113,7 +113,7 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
 // copies (one mbarrier a stage); warps meet once, to add up their partial results.
 // Bound by issue, some 385 instructions for 16 tokens of both kinds at 4 bits (codes to operands, MMAs that fill 4
 // of 8 columns, one softmax over 32 tokens at a time), and by some 10 us of launch, first loads and merge: one token
-// of four sequences of 64K to 40K, 8 KV heads, takes 67.4 us with the merge (232 MB, 3.4 TB/s; each further token
+// of four sequences of 64K to 40K, 8 KV heads, takes 66.5 us with the merge (232 MB, 3.4 TB/s; each further token
 // costs what 4.4 TB/s would), issue slots 58% busy at two blocks of 125 registers an SM.
 template <typename T, int D, int NT, bool PACK>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeArgs a) {
@@ -635,9 +635,9 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
   TreePlan t{};
   const int rows = n_new * (n_q / p.n_kv);
   // tcgen05 pays for 128 rows whatever their number, mma.sync for each 16. Four ragged sequences of up to 8192
-  // tokens, 8 KV heads, tcgen05 against mma.sync: 16 rows 36.9 and 26.8 us, 32 rows 38.4 and 43.2, 64 rows 40
-  // and 84; one sequence of 131072: 16 rows 113.5 and 69.2 us, 32 rows 114.6 and 123.2; 32 rows over 512
-  // tokens 18.8 and 22.2.
+  // tokens, 8 KV heads, tcgen05 against mma.sync: 16 rows 34.1 and 26.8 us, 32 rows 34.6 and 43.2, 64 rows 36.3
+  // and 84; one sequence of 131072: 16 rows 103 and 69.2 us, 32 rows 103 and 123.2; 32 rows over 512 tokens
+  // 17.0 and 22.2.
   if (rows > 16 && p.io_dtype == JOLT_BF16) {
     t.tc = true;
     t.blocks = (rows + 127) / 128;

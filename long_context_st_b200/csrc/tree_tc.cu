@@ -15,10 +15,10 @@
 // Features stand in the order in which the widening leaves them; R q is laid out to match, and the merge puts
 // the outputs back.
 //
-// 256 query rows over 131072 tokens, 8 KV heads: 210 us with the merge, 0.65 PFLOP/s of the two products (the keys'
-// second term makes it 1.0 of MMA work; tensor pipe 44% busy, issue slots 57%). The roles alone take 133 us (widening),
-// 115 (MMAs, whose operands share the shared memory with it) and 93 (softmax); together they wait for one another
-// at a tile's end. Each block of 128 rows widens the codes for itself.
+// 256 query rows over 131072 tokens, 8 KV heads: 190 us with the merge, 0.72 PFLOP/s of the two products (the keys'
+// second term makes it 1.1 of MMA work; tensor pipe 48% busy). The roles alone take 115 us (MMAs, whose operands
+// share the shared memory with the widening's stores), 93 (softmax) and as much (widening); together they wait for
+// one another at a tile's end. Each block of 128 rows widens the codes for itself.
 #include <cuda.h>
 
 #include <algorithm>
