@@ -138,6 +138,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   const int rows = min(RB, cnt * a.gq - r0);
   if (rows <= 0) return;
 
+  // this warp's rows of q, on their way while the first tiles are asked for
+  constexpr int kPer = (RB + kWarps - 1) / kWarps;
+  float v[kPer][E];
+  {
+    const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = warp + i * kWarps;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+      if (r < rows) {
+        const T* x = qb + q_offset(a, r0 + r, D) + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = ld_as_float(x, e);
+      }
+    }
+  }
+
   uint2* qf = reinterpret_cast<uint2*>(smem);                        // [QT][NT][NS][32]
   float* qsum = reinterpret_cast<float*>(qf + QT * NT * NS * 32);    // [C]
   float* xm = qsum + C;                                              // [kWarps][C]
@@ -194,11 +212,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
   // that the codes of quarter row m give at that step. One power of two for all rows.
   float unscale;
   {
-    const T* qb = static_cast<const T*>(a.q) + int64_t(b) * a.qsb + int64_t(h) * a.gq * D;
     const float isd = rsqrtf(float(D));
     __half* qh = reinterpret_cast<__half*>(qf);
-    constexpr int kPer = (RB + kWarps - 1) / kWarps;
-    float v[kPer][E], top = 0.f;
+    float top = 0.f;
     float sign[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) sign[e] = rot_sign(a.p.seed, lane * E + e) * a.scale2;
@@ -206,12 +222,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
     for (int i = 0; i < kPer; ++i) {
       const int r = warp + i * kWarps;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-      if (r < rows) {
-        const T* x = qb + q_offset(a, r0 + r, D) + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[i][e] = ld_as_float(x, e) * sign[e];
-      }
+      for (int e = 0; e < E; ++e) v[i][e] *= sign[e];
       if (lane == 0 && r < RB) {  // the elements of H x add up to D x_0
         qsum[r] = v[i][0] * (float(D) * isd);
         if (PACK) qsum[r + 4] = qsum[r];
@@ -465,7 +476,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         xl[warp * C + col] = l[nt][c] * f;
         xz[warp * C + col] = z[nt][c] * f;
       }
-      ref[nt][c] = top;
       const float off = kWhole ? 0.f : ov_off * o[NS][nt][c];
 #pragma unroll
       for (int mt = 0; mt < NS; ++mt) {
@@ -477,44 +487,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeAr
         }
       }
     }
-  float* red = reinterpret_cast<float*>(ring0);  // [kWarps / 2][NS * NT * 4][32]
+  // every warp leaves its sums, and adds up some of them over the warps: four features of a column a group
+  float* red = reinterpret_cast<float*>(ring0);  // [kWarps][NS * NT * 4][32]
   constexpr int NR = NS * NT * 4;
 #pragma unroll
-  for (int half = kWarps / 2; half >= 1; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
+  for (int i = 0; i < NR; ++i) red[(warp * NR + i) * 32 + lane] = o[i / (NT * 4)][(i / 4) % NT][i % 4];
+  __syncthreads();
+#pragma unroll 1
+  for (int q = warp; q < NS * NT; q += kWarps) {
+    const int mt = 2 * (q % (NS / 2)), nt = q / NS, c = q / (NS / 2) % 2, col = nt * 8 + 2 * m + c;
+    if (col >= rows) continue;
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, ls = 0.f, zs = 0.f, top = -INFINITY;
+    const float* from = red + (mt * NT * 4 + nt * 4 + c) * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) red[((warp - half) * NR + i) * 32 + lane] = o[i / (NT * 4)][(i / 4) % NT][i % 4];
-    }
-    __syncthreads();
-    if (warp < half) {
+    for (int w = 0; w < kWarps; ++w) {
 #pragma unroll
-      for (int i = 0; i < NR; ++i) o[i / (NT * 4)][(i / 4) % NT][i % 4] += red[(warp * NR + i) * 32 + lane];
+      for (int i = 0; i < 4; ++i) x[i] += from[(w * NR + (i >> 1) * NT * 4 + (i & 1) * 2) * 32];
+      top = fmaxf(top, xm[w * C + col]);
+      ls += xl[w * C + col];
+      zs += xz[w * C + col];
     }
-    __syncthreads();
+    const int64_t part = out_row(a, b, h, r0 + col) * a.parts + split;
+    if (g == 0 && mt == 0) a.ml[part] = make_float2(top, ls);
+    if (top != -INFINITY)
+      *reinterpret_cast<float4*>(a.acc + part * D + g * (D / 8) + 2 * mt) = make_float4(x[0] + zs, x[1] + zs, x[2] + zs, x[3] + zs);
   }
-  if (warp != 0) return;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = nt * 8 + 2 * m + c;
-      if (col >= rows) continue;
-      float ls = 0.f, zs = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        ls += xl[w * C + col];
-        zs += xz[w * C + col];
-      }
-      const int row = r0 + col;
-      const int64_t part = out_row(a, b, h, row) * a.parts + split;
-      if (g == 0) a.ml[part] = make_float2(ref[nt][c], ls);
-      if (ref[nt][c] == -INFINITY) continue;
-      float* dst = a.acc + part * D + g * (D / 8);
-#pragma unroll
-      for (int mt = 0; mt < NS; mt += 2)
-        *reinterpret_cast<float4*>(dst + 2 * mt) = make_float4(o[mt][nt][c] + zs, o[mt][nt][c + 2] + zs,
-                                                               o[mt + 1][nt][c] + zs, o[mt + 1][nt][c + 2] + zs);
-    }
 }
 
 // One warp a row: joins the splits, rotates their sum back, then adds the drafted tokens' part and the
@@ -654,7 +651,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
     const int C = 8 * t.nt, qt = t.pack ? 1 : 2;
     const size_t head = size_t(qt) * t.nt * (p.d_h / 16) * 256 + C * 4 + 3 * kWarps * C * 4 + kWarps * kMaxStages * 12;
     const size_t ring = size_t(kWarps) * t.stages * t.stage_bytes;
-    const size_t red = size_t(kWarps / 2) * (p.d_h / 16) * t.nt * 4 * 128;
+    const size_t red = size_t(kWarps) * (p.d_h / 16) * t.nt * 4 * 128;
     const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
     t.smem = std::max(head + std::max(ring, red), draft);
   }
