@@ -110,11 +110,11 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
 // as their 16 rows and query rows as their 8 columns, so single-token decoding wastes little; with
 // PACK (at most 4 rows) columns 0-3 carry the first term of R q and 4-7 the second, and the values
 // the two terms of p likewise. Each warp takes 32-token tiles of its own through a ring of bulk
-// copies (one mbarrier a stage); warps meet once, to add up their partial results.
+// copies (one mbarrier a stage); the warps meet at the end, to add up their partial results.
 // Bound by issue, some 385 instructions for 16 tokens of both kinds at 4 bits (codes to operands, MMAs that fill 4
 // of 8 columns, one softmax over 32 tokens at a time), and by some 10 us of launch, first loads and merge: one token
-// of four sequences of 64K to 40K, 8 KV heads, takes 66.5 us with the merge (232 MB, 3.4 TB/s; each further token
-// costs what 4.4 TB/s would), issue slots 58% busy at two blocks of 125 registers an SM.
+// of four sequences of 64K to 40K, 8 KV heads, takes 65.7 us with the merge (232 MB, 3.5 TB/s; each further token
+// costs what 4.4 TB/s would), issue slots 60% busy at two blocks of 126 registers an SM.
 template <typename T, int D, int NT, bool PACK>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeArgs a) {
   using namespace sm100;
