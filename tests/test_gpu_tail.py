@@ -448,6 +448,15 @@ def test_attention_reports_bad_pages_and_lengths(cuda_ok):
     del want
 
 
+@pytest.mark.parametrize("io,n,nq", [("f32", 1, 1), ("bf16", 1, 1), ("bf16", 9, 2), ("f32", 9, 2)])
+@pytest.mark.parametrize("batch,nkv", [(24, 16), (100, 1), (130, 1)])
+def test_attention_many_sequences(cuda_ok, io, n, nq, batch, nkv):
+    """Batches that are divided evenly over the GPU and batches with a block of its own for every sequence,
+    some of them empty."""
+    lens = [(37 * i) % 300 if i % 5 else 0 for i in range(batch)]
+    check_case(attn_case(batch, lens, n, nq * nkv, nkv, 64, 4, 4, 16, io, counts=[n - (i % 3 == 2) for i in range(batch)]))
+
+
 def test_attention_scales_far_apart(cuda_ok):
     """Value scales over fp16's whole range, constant rows, and rows whose first tile is empty of scale."""
     for io in ("f32", "bf16"):
