@@ -497,7 +497,11 @@ size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t 
  *   ws       device, >= jolt_tree_attn_workspace, 256-byte aligned, its first 4 bytes zero before the
  *            first call (the error word, read by jolt_check); calls sharing a ws must not overlap in time
  * Scores and softmax statistics are fp32. bf16 with more than 16 query rows (n_new * n_q / n_kv) runs its
- * products on tcgen05, the rest on m16n8k16 MMAs. Asynchronous on `stream`. */
+ * products on tcgen05, the rest on m16n8k16 MMAs. What goes into the products in fewer bits than fp32's 24: R q in 22;
+ * the weights in 11 for bf16 (22 for fp32; 16 over the drafted tokens' values), with tcgen05 the values in 11 too.
+ * So a bf16 output is off by its own rounding (2^-9 of a row's norm in the mean) and some 2^-11 of the root of the
+ * summed squares of weight times value. A value row some 2^15 times the others (2^13 where fp32 tensors' 22 bits
+ * count) costs them bits, whatever its weight. Asynchronous on `stream`. */
 jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
                            const int32_t* lens, int32_t batch, int32_t n_new, int32_t n_q, const int32_t* counts,
                            const uint64_t* mask, const void* q, int64_t q_stride_b, int64_t q_stride_t,

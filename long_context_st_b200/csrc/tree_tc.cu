@@ -1,5 +1,6 @@
-// jolt_tree_attn for bf16 and more than 16 query rows a KV head: the products on tcgen05 (see tree_attn.cu
-// for the arithmetic, which is the same).
+// jolt_tree_attn for bf16 and more than 16 query rows a KV head: the products on tcgen05. Scores as in
+// tree_attn.cu; p is one f16 term, and the values are widened to f16 themselves (kVExp below), where tree_attn.cu
+// takes their codes whole and their scales into p.
 //
 // A block takes 128 query rows (drafted token x head of the group) of one KV head and a range of the
 // sequence's pages, 128 tokens a tile. Query rows are the MMA's M, so a row's softmax stays with one
@@ -41,11 +42,23 @@ constexpr float kPExp = 7.f;     // p is carried times 2^7
 constexpr float kRoom = 4.f;     // how far above a row's maximum its reference is set
 constexpr float kMost = 32768.f;  // and a thread's sum of eight of them below 2^15, so that each is within f16
 // A value is taken from its code's bits as an f16 number c 2^-24 by one multiply-add, whose factor has to be
-// an f16 number too: values are carried times 2^(kVExp - ve), so that a scale of at most 2^(ve + 1 - b) gives
-// at most 2^15.5. They then reach 2^(b - 10), and besides f16's 2^-12 are off by at most 2^-25, 2^-(15 + b)
-// of the largest value met.
+// an f16 number too: a token's values are carried times 2^(kVExp - e), 2^e being above all of them, so that a
+// scale of at most 2^(e + 1 - b) gives at most 2^15.5. They then reach 2^(b - 10), and besides f16's 2^-11 are off by
+// at most 2^-25, 2^-(15 + b) of 2^e. The outputs are kept in one unit for all tokens, 2^(ve - kVExp) with ve the
+// largest such exponent met so far. A token within 2^kNear of it takes ve for its e (off by 2^-(11 + b) of its largest at
+// most, below the 2^-11); any other its own, and its p goes in times 2^(e - ve). A large value row so takes
+// nothing from the others' bits, whatever its weight, until it is some 2^15 times as large (p then leaves f16's
+// normal range). One unit for all values put errors of 2^-(15 + b) of the largest row into every one: 2% of the
+// output at 2 bits where a row without weight was 2^12 times the others. Without kNear, and with the product on p
+// made as p is formed, every tile pays for what few need: 204 us at 256 rows over 131072 tokens, 198 as it is, 193 with
+// one unit for all.
+constexpr int kNear = 3;
 template <int BV>
 constexpr int kVExp = BV - 10;
+__device__ __forceinline__ int value_exp(float scale, float zero, float levels) {
+  const float top = fmaxf(fabsf(zero), fabsf(__fmaf_rn(levels, scale, zero)));
+  return min(max(int(__float_as_uint(top) >> 23) - 126, -30), 30);
+}
 
 template <int D>
 struct Smem {
@@ -55,13 +68,16 @@ struct Smem {
   static constexpr int k = q + 2 * kTile;          // two buffers
   static constexpr int v = k + 2 * kTile;          // two buffers
   static constexpr int sc = v + 2 * kTile;         // [4][64 token pairs][4] floats: key scales, key zeros
-  static constexpr int rs = sc + 4 * 64 * 16;      // [26] warps' largest |R q|
+  static constexpr int pe = sc + 4 * 64 * 16;      // [4][64 token pairs] f16 pairs: what p is multiplied by, 2^(e - ve)
+  static constexpr int own = pe + 4 * 64 * 4;      // [4][128] what values are multiplied by for it, 2^(ve - e)
+  static constexpr int rs = own + 4 * 128 * 4;     // [26] warps' largest |R q|
   static constexpr int qs = rs + 128;              // [128] sum(R q)
   static constexpr int ref = qs + 512;             // [128] the rows' references as the last finished tile left them
   static constexpr int l = ref + 512;              // [128] the odd tiles' sums
   static constexpr int vis = l + 512;              // [4][4] words: visible tokens
   static constexpr int ve = vis + 64;              // [4][2] value exponent of this tile and of the one before
-  static constexpr int bars = ve + 32;             // 23 mbarriers
+  static constexpr int far = ve + 32;              // [4] whether some token's unit is not ve
+  static constexpr int bars = far + 16;            // 23 mbarriers
   static constexpr int slot = bars + 192;          // tensor memory base
   static constexpr int work = slot + 16;           // Work, rows
   static constexpr int un = work + 48;             // power of two of the scores' accumulators
@@ -154,8 +170,8 @@ __device__ __forceinline__ void widen_keys(const uint32_t (&w)[D * B / 128], uin
     *reinterpret_cast<uint4*>(tile + off[i]) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
-// Values: dequantised, code * scale + zero in f16 by one fused multiply-add from the field's bits, in units of
-// 2^(ve - kVExp): scale[F] holds scale * 2^(24 - place) for the F places of a field in its byte.
+// Values: dequantised, code * scale + zero in f16 by one fused multiply-add from the field's bits, in the token's
+// units of 2^(e - kVExp): scale[F] holds scale * 2^(24 - place) for the F places of a field in its byte.
 template <int D, int B>
 __device__ __forceinline__ void widen_values(const uint32_t (&w)[D * B / 128], float2 sz, uint8_t* tile,
                                              const int (&off)[D / 32]) {
@@ -272,9 +288,9 @@ __device__ void keys_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane) 
   }
 }
 
-// Warp 25: per token pair the keys' (scale, zero) as the softmax uses them, which tokens are seen, and the
-// exponent of the values' largest magnitude so far (ve): values are widened in units of 2^(ve - kVExp).
-// Four tokens a lane.
+// Warp 25: per token pair the keys' (scale, zero) as the softmax uses them, which tokens are seen, the exponent of
+// the values' largest magnitude so far (ve), and the power of two from each token's own exponent to it. Four
+// tokens a lane.
 template <int D>
 __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
   using S = Smem<D>;
@@ -307,14 +323,16 @@ __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
     // tile n - 4 is done with this place, the widening of its values among it
     if (n >= 4 && !wait_all(c.pv_done(n - 4), ((n - 4) >> 2) & 1, a.err)) return;
     const uint32_t ku[4] = {kz.x, kz.y, kz.z, kz.w}, vu[4] = {vz.x, vz.y, vz.z, vz.w};
-    float sc[4], ze[4], most = 0.f;
+    float sc[4], ze[4];
+    int e[4], most = -30;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 k = h2_floats(ku[i]), v = h2_floats(vu[i]);
       const bool here = (seen >> i) & 1;
       sc[i] = here ? k.x * unscale : 0.f;
       ze[i] = here ? k.y + ko * k.x : 0.f;
-      if (here) most = fmaxf(most, fmaxf(fabsf(v.y), fabsf(v.y + vtop * v.x)));
+      e[i] = here ? value_exp(v.x, v.y, vtop) : -30;
+      most = max(most, e[i]);
     }
     float4* dst = reinterpret_cast<float4*>(c.smem + S::sc + q * 1024) + lane * 2;
     dst[0] = make_float4(sc[0], sc[1], ze[0], ze[1]);
@@ -324,10 +342,27 @@ __device__ void scales_role(const TreeArgs& a, const Ctx<D>& c, int lane) {
 #pragma unroll
     for (int x = 1; x <= 4; x <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, x);
     if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(c.smem + S::vis)[q * 4 + (lane >> 3)] = word;
-    const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     const int before = ve;
-    ve = min(max(ve, int(big >> 23) - 126), 30);
-    if (lane == 0) reinterpret_cast<int2*>(c.smem + S::ve)[q] = make_int2(ve, n ? before : ve);
+    ve = max(ve, __reduce_max_sync(0xffffffffu, most));
+    bool far = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!((seen >> i) & 1) || e[i] >= ve - kNear) e[i] = ve;
+      far = far || e[i] != ve;
+    }
+    far = __any_sync(0xffffffffu, far);
+    if (far) {  // f16 has powers of two down to 2^-24
+      uint2 up;
+      up.x = h2_pack(pow2i(e[0] - ve), pow2i(e[1] - ve));
+      up.y = h2_pack(pow2i(e[2] - ve), pow2i(e[3] - ve));
+      reinterpret_cast<uint2*>(c.smem + S::pe + q * 256)[lane] = up;
+      reinterpret_cast<float4*>(c.smem + S::own + q * 512)[lane] =
+          make_float4(pow2i(ve - e[0]), pow2i(ve - e[1]), pow2i(ve - e[2]), pow2i(ve - e[3]));
+    }
+    if (lane == 0) {
+      reinterpret_cast<int2*>(c.smem + S::ve)[q] = make_int2(ve, n ? before : ve);
+      reinterpret_cast<int*>(c.smem + S::far)[q] = far;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(c.sc_full(n));
     if (n + 1 < c.n_tiles) fetch(n + 1);
@@ -371,12 +406,21 @@ __device__ void values_role(const TreeArgs& a, const Ctx<D>& c, int wq, int lane
   for (int n = 0; n < c.n_tiles; ++n) {
     const int s = n & 1;
     if (!wait_all(c.sc_full(n), (n >> 2) & 1, a.err)) return;  // ve of this tile
-    const float down = pow2i(kVExp<BV> - reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3].x);
+    const bool far = reinterpret_cast<const int*>(c.smem + S::far)[n & 3];
+    const float unit = pow2i(kVExp<BV> - reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3].x);
     float2 sz[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const float2 f = __half22float2(raw[it]);
-      sz[it] = (seen >> it) & 1 ? make_float2(f.x * (down * 16777216.f), f.y * down) : make_float2(0.f, 0.f);
+      sz[it] = (seen >> it) & 1 ? make_float2(f.x * (unit * 16777216.f), f.y * unit) : make_float2(0.f, 0.f);
+    }
+    if (far) {
+      const float* own = reinterpret_cast<const float*>(c.smem + S::own) + (n & 3) * 128 + wq * 32 + g;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        sz[it].x *= own[it * 8];
+        sz[it].y *= own[it * 8];
+      }
     }
     const bool more = n + 1 < c.n_tiles;
     if (more) pages(n + 1);
@@ -481,8 +525,9 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
     const uint32_t* vis = reinterpret_cast<const uint32_t*>(c.smem + S::vis) + (n & 3) * 4;
     const int2 ve = reinterpret_cast<const int2*>(c.smem + S::ve)[n & 3];
     const bool whole = (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu;
-    // this tile's P of chunks [0, end) times f
-    auto scale_p = [&](float f0, float f1, int end) {
+    // this tile's P of chunks [0, end) times f, and into the unit of the outputs (far)
+    auto scale_p = [&](float f0, float f1, int end, bool far) {
+      const __half2* pe = reinterpret_cast<const __half2*>(c.smem + S::pe + (n & 3) * 256) + m;
       tmem_st_wait();
 #pragma unroll 1
       for (int e = 0; e < end; ++e) {
@@ -491,7 +536,8 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn((i & 1) ? f1 : f0));
+          __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[i]), __float2half2_rn((i & 1) ? f1 : f0));
+          if (far) v = __hmul2(v, pe[(e * 4 + (i >> 1)) * 4]);
           y[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
         st_16x128(ts + e * 32, y);
@@ -561,7 +607,7 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
           f[r] = raise(r, fmaxf(ref[r], ceilf(top[r]) + kRoom));
         }
-        scale_p(f[0], f[1], ch);
+        scale_p(f[0], f[1], ch, false);
         continue;
       }
       tried = false;
@@ -570,13 +616,17 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
       st_16x128(ts + ch * 32, pk);
       ++ch;
     }
+    // tokens whose values are in units of their own, and the references that tile n - 1 ended with
+    const bool far = reinterpret_cast<const int*>(c.smem + S::far)[n & 3];
+    float fp[2] = {1.f, 1.f};
+    bool p_too = far;
     if (n > 0) {
       // the references that tile n - 1 ended with, and O, which is in their and its values' units
       ok = wait_all(c.p_full(n - 1), ((n - 1) >> 2) & 1, a.err);
       if (!ok) break;
       const float drop = pow2i(max(ve.y - ve.x, -126));
-      float fp[2], fo[2];
-      bool p_too = false, o_too = drop != 1.f;
+      float fo[2];
+      bool o_too = drop != 1.f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float was = ref_s[8 * r];
@@ -586,7 +636,6 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
         o_too = o_too || now != was;
         fp[r] = raise(r, now);
       }
-      if (__any_sync(0xffffffffu, p_too)) scale_p(fp[0], fp[1], 4);
       if (__any_sync(0xffffffffu, o_too)) {
         ok = wait_all(c.pv_done(n - 1), ((n - 1) >> 2) & 1, a.err);
         if (!ok) break;
@@ -602,6 +651,7 @@ __device__ void softmax_role(const TreeArgs& a, const Ctx<D>& c, uint32_t tmem, 
         }
       }
     }
+    if (__any_sync(0xffffffffu, p_too)) scale_p(fp[0], fp[1], 4, far);
     if (m == 0) {
       ref_s[0] = ref[0];
       ref_s[8] = ref[1];
