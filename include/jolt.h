@@ -472,7 +472,8 @@ jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool, const int
  * is i or an ancestor of i. n <= 64. JOLT_ERR_INVALID_ARG on a parent that is not earlier. */
 jolt_status jolt_tree_mask(const int32_t* parents, int32_t n, uint64_t* mask);
 
-/* Workspace bytes of jolt_tree_attn (0 on bad arguments). */
+/* Workspace bytes of jolt_tree_attn (0 on bad arguments): enough for every call with these pages and n_q and at most
+ * this batch, n_new and max_pages. */
 size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t n_new, int32_t n_q,
                                 int32_t max_pages);
 

@@ -499,6 +499,7 @@ def tree_mask(parents):
 
 
 def new_tree_workspace(p: Pages, batch, n_new, n_q, max_pages, device="cuda"):
+    """Workspace of tree_attn for every call of at most this batch, n_new and max_pages."""
     n = int(lib().jolt_tree_attn_workspace(C.byref(p), batch, n_new, n_q, max_pages))
     if n == 0:
         raise JoltError(-1, "jolt_tree_attn_workspace")

@@ -726,7 +726,16 @@ using namespace jolt;
 extern "C" size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t n_new, int32_t n_q,
                                            int32_t max_pages) {
   if (!tree_dims_ok(pages, batch, n_new, n_q, max_pages)) return 0;
-  return tree_plan(*pages, std::max(batch, 1), std::max(n_new, 1), n_q, max_pages).ws_total;
+  // What any call of at most these sizes takes. A larger batch or tree can take less: blocks of more rows, or of more
+  // sequences than there are shares, leave fewer splits. For a tree size the most is at the given batch, or at the
+  // largest that is still divided evenly; wider tables only add splits.
+  size_t most = 0;
+  for (int n = 1; n <= std::max(n_new, 1); ++n) {
+    int even = std::min(batch, kMaxBalanced);
+    while (even > 1 && !tree_plan(*pages, even, n, n_q, max_pages).balanced) --even;
+    for (int b : {std::max(batch, 1), std::max(even, 1)}) most = std::max(most, tree_plan(*pages, b, n, n_q, max_pages).ws_total);
+  }
+  return most;
 }
 
 extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table,

@@ -45,3 +45,18 @@ def test_large_values_without_weight_cost_the_others_nothing(cuda_ok, n, io, d, 
     own = (ref[0].to(out.dtype).double() - ref[0]).norm(dim=-1)
     before = (ref[2] - HALF[out.dtype] * norm) / 3
     assert float(err.square().mean()) <= float((own.square() + before.square()).mean())
+
+
+def test_one_workspace_serves_every_smaller_call(cuda_ok):
+    """A workspace made once for the largest batch and tree, whatever earlier calls left in it."""
+    p0 = api.make_pages(1, 16, 8, 64, 4, 4)
+    ws = api.new_tree_workspace(p0, 40, 20, 16, 60)
+    ws[256:] = 0xFF
+    for batch, n, width in ((40, 20, 60), (38, 1, 60), (37, 1, 60), (19, 9, 31), (18, 9, 60), (16, 2, 60), (5, 20, 60), (1, 1, 1)):
+        lens = [(1 + 611 * i) % (16 * width) for i in range(batch)]
+        c = attn_case(batch + n, lens, n, 16, 8, 64, 4, 4, 16, "bf16")
+        t = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+        t[:, :c[2].shape[1]] = c[2][:, :width]
+        c = c[:2] + (t,) + c[3:]
+        got, want = run_attn(c, ws=ws), run_attn(c)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

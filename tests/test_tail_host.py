@@ -177,3 +177,29 @@ def test_quotient_by_reciprocal_gives_the_divisions_codes():
             got = np.where(near | out, want, c)
             assert np.array_equal(np.abs(got), want)
             assert near.mean() < 1e-3 or a is not some
+
+
+@pytest.mark.parametrize("over", [dict(n_kv=8), dict(n_kv=8, io_dtype="f32"), dict(n_kv=1, d_h=64), dict(n_kv=40)])
+def test_a_workspace_serves_every_smaller_call(over):
+    """One workspace for the largest batch and tree: sequences finish, trees shrink, tables may be narrower. The
+    splits a call makes depend on all three (37 and 38 sequences of 8 KV heads, 18 and 19 of larger trees, 8 and 9, 16
+    and 17, 128 and 129 query rows fall on different sides of a rule)."""
+    p = api.make_pages(**(PAGES | over))
+
+    def size(batch, n_new, g, pages=1024):
+        return _lib.lib().jolt_tree_attn_workspace(C.byref(p), batch, n_new, g * p.n_kv, pages)
+
+    batches = [1, 2, 3, 5, 9, 16, 18, 19, 36, 37, 38, 64, 127, 128, 129, 148, 149, 296, 297, 400]
+    for g in (1, 4, 8):
+        for trees in ([1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64],):
+            last = {}
+            for b in batches:
+                for n in trees:
+                    got = size(b, n, g)
+                    assert got > 0
+                    for key in ((batches[batches.index(b) - 1], n) if b > 1 else None,
+                                (b, trees[trees.index(n) - 1]) if n > 1 else None):
+                        assert key is None or last[key] <= got, (b, n, g, key)
+                    last[b, n] = got
+        for pages in (1, 2, 5, 100, 1023):
+            assert size(16, 4, g, pages) <= size(16, 4, g, pages + 1)
