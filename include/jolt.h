@@ -460,8 +460,9 @@ jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, const int32_t
  * lens[s], into row i of k_out and v_out; other rows are left as they were.
  *   start    device int32 [batch] >= 0 (NULL: 0; a negative one is an error and reads nothing)
  *   k_out, v_out  device [batch][n_kv][n_out][d_h] io dtype, rows contiguous, element strides stride_b
- *            (sequence) and stride_h (head), multiples of 8 and at least n_out*d_h (where there are
- *            several), 16-byte aligned; either may be NULL. With a
+ *            (sequence) and stride_h (head), multiples of 8, 16-byte aligned; either may be NULL. No two
+ *            rows may share memory: one stride is at least n_out*d_h, the other at least the
+ *            extent of what that one counts. With a
  *            layer's strides of jolt_compress's K and V this folds a tail into a stored cache's input.
  * Asynchronous on `stream`. */
 jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,

@@ -546,9 +546,14 @@ extern "C" jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool
   if (batch == 0 || n_out == 0) return JOLT_OK;
   if ((!k_out && !v_out) || !rows_ok(k_out, stride_b, stride_h) || !rows_ok(v_out, stride_b, stride_h))
     return JOLT_ERR_INVALID_ARG;
-  // rows of different heads or sequences must not fall on one another
-  const int64_t row = int64_t(n_out) * pages->d_h;
-  if ((pages->n_kv > 1 && stride_h < row) || (batch > 1 && stride_b < row)) return JOLT_ERR_INVALID_ARG;
+  // rows of different heads or sequences must not fall on one another: the heads' lie between the sequences', or
+  // the other way round
+  const int64_t row = int64_t(n_out) * pages->d_h, nh = pages->n_kv;
+  auto nested = [row](int64_t inner, int64_t n_inner, int64_t outer, int64_t n_outer) {
+    return (n_inner == 1 || inner >= row) &&
+           (n_outer == 1 || (outer >= row && (n_inner == 1 || (outer - row) / (n_inner - 1) >= inner)));
+  };
+  if (!nested(stride_h, nh, stride_b, batch) && !nested(stride_b, batch, stride_h, nh)) return JOLT_ERR_INVALID_ARG;
   ReadArgs a{};
   a.p = pages_dev(*pages, pool, table, max_pages, lens);
   a.out[0] = k_out;

@@ -203,3 +203,15 @@ def test_a_workspace_serves_every_smaller_call(over):
                     last[b, n] = got
         for pages in (1, 2, 5, 100, 1023):
             assert size(16, 4, g, pages) <= size(16, 4, g, pages + 1)
+
+
+def test_read_refuses_rows_that_fall_on_one_another():
+    """Sequences and heads may be nested either way round, but no two rows may share memory."""
+    p = api.make_pages(**PAGES)  # 2 KV heads of 128
+    row = 3 * 128
+
+    def read(sb, sh, batch=4):
+        return _lib.lib().jolt_pages_read(C.byref(p), FAKE, FAKE, 4, FAKE, batch, None, 3, FAKE, FAKE, sb, sh, None, None)
+
+    for sb, sh in ((row, row), (row, 2 * row), (2 * row - 8, row), (row, 4 * row - 8), (row + 8, row + 16)):
+        assert read(sb, sh) == BAD, (sb, sh)
