@@ -421,7 +421,7 @@ jolt_status jolt_decode_attn_noalloc(const jolt_shape* shape, const jolt_cell_ch
  * Device-side checks: a length outside [0, max_pages*page_size] is clamped (reads, attention) or leaves the
  * sequence unwritten (append), a table entry outside [0, n_pages) makes its page's tokens invisible or
  * unwritten; both set JOLT_ERR_INVALID_ARG in the error word. err (device int32, may be NULL) as in
- * jolt_quantize_pack: set, never cleared. batch is at most 65535; a call
+ * jolt_quantize_pack: set, never cleared. Arrays are aligned to their elements (masks to 8 bytes). batch is at most 65535; a call
  * with batch, n_new or n_out 0 returns JOLT_OK. */
 typedef struct {
   int32_t n_pages;      /* pages in the pool >= 1 */

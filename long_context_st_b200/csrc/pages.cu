@@ -490,7 +490,7 @@ bool pool_args_ok(const jolt_pages* p, const void* pool, const int32_t* table, i
   if (!pages_ok(p) || max_pages < 1 || batch < 0 || batch > 65535) return false;
   if (int64_t(max_pages) * p->page_size > (int64_t(1) << 24)) return false;
   if (batch == 0) return true;
-  return pool && table && lens && reinterpret_cast<uintptr_t>(pool) % 16 == 0;
+  return pool && table && lens && aligned(pool, 16) && aligned(table, 4) && aligned(lens, 4);
 }
 bool rows_ok(const void* x, int64_t s0, int64_t s1) {
   return reinterpret_cast<uintptr_t>(x) % 16 == 0 && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
@@ -510,6 +510,7 @@ extern "C" jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, co
   if (batch == 0 || n_new == 0) return JOLT_OK;
   if (!k || !v || (!src && n_new > n_src) || !rows_ok(k, stride_b, stride_t) || !rows_ok(v, stride_b, stride_t))
     return JOLT_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(src, 4) || !aligned(err, 4)) return JOLT_ERR_INVALID_ARG;
   const int64_t rows = int64_t(batch) * n_new * pages->n_kv;
   if (rows >= int64_t(1) << 31) return JOLT_ERR_INVALID_ARG;
   AppendArgs a{};
@@ -546,6 +547,7 @@ extern "C" jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool
   if (batch == 0 || n_out == 0) return JOLT_OK;
   if ((!k_out && !v_out) || !rows_ok(k_out, stride_b, stride_h) || !rows_ok(v_out, stride_b, stride_h))
     return JOLT_ERR_INVALID_ARG;
+  if (!aligned(start, 4) || !aligned(err, 4)) return JOLT_ERR_INVALID_ARG;
   // rows of different heads or sequences must not fall on one another: the heads' lie between the sequences', or
   // the other way round
   const int64_t row = int64_t(n_out) * pages->d_h, nh = pages->n_kv;

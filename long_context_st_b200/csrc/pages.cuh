@@ -7,6 +7,7 @@
 namespace jolt {
 
 bool pages_ok(const jolt_pages* p);
+inline bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }  // NULL is
 
 // Byte offsets of a page's segments and its size.
 struct PageLayout {

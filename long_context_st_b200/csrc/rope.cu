@@ -234,7 +234,8 @@ extern "C" jolt_status jolt_rope(const void* q, void* q_out, int32_t n_q, int64_
   if (!(scaling - scaling == 0.f) || (inverse != 0 && inverse != 1)) return JOLT_ERR_INVALID_ARG;
   if (n_tokens == 0) return JOLT_OK;
   if (!pos || !inv_freq || (n_q && (!q || !q_out)) || (n_kv && (!k || !k_out))) return JOLT_ERR_INVALID_ARG;
-  if (n_tokens > (int64_t(1) << 31)) return JOLT_ERR_INVALID_ARG;
+  if (n_tokens > (int64_t(1) << 31) || reinterpret_cast<uintptr_t>(pos) % 4 || reinterpret_cast<uintptr_t>(inv_freq) % 4)
+    return JOLT_ERR_INVALID_ARG;
   RopeArgs a{};
   a.t[0] = RopeTensor{q, q_out, q_stride, q_out_stride, n_q};
   a.t[1] = RopeTensor{k, k_out, k_stride, k_out_stride, n_kv};

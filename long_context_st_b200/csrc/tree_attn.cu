@@ -748,9 +748,11 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   if (!tree_dims_ok(pages, batch, n_new, n_q, max_pages)) return JOLT_ERR_INVALID_ARG;
   if (!(attn_scale > 0.f) || !(attn_scale < INFINITY)) return JOLT_ERR_INVALID_ARG;
   if (batch == 0 || n_new == 0) return JOLT_OK;
-  if (!pool || reinterpret_cast<uintptr_t>(pool) % 16 || !table || !lens || !q || !out || !ws)
+  if (!pool || !table || !lens || !q || !out || !ws) return JOLT_ERR_INVALID_ARG;
+  if (!aligned(pool, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(counts, 4) || !aligned(mask, 8) ||
+      !aligned(prefix_out, pages->io_dtype == JOLT_F32 ? 4 : 2) || !aligned(prefix_lse, 4) || !aligned(lse, 4) ||
+      !aligned(out, 16) || !aligned(ws, 256))
     return JOLT_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(out) % 16 || reinterpret_cast<uintptr_t>(ws) % 256) return JOLT_ERR_INVALID_ARG;
   if (!rows_ok(q, q_stride_b, q_stride_t) || (!k != !v) || (!prefix_out != !prefix_lse)) return JOLT_ERR_INVALID_ARG;
   if (k && (!rows_ok(k, kv_stride_b, kv_stride_t) || !rows_ok(v, kv_stride_b, kv_stride_t))) return JOLT_ERR_INVALID_ARG;
   const TreePlan t = tree_plan(*pages, batch, n_new, n_q, max_pages);

@@ -215,3 +215,26 @@ def test_read_refuses_rows_that_fall_on_one_another():
 
     for sb, sh in ((row, row), (row, 2 * row), (2 * row - 8, row), (row, 4 * row - 8), (row + 8, row + 16)):
         assert read(sb, sh) == BAD, (sb, sh)
+
+
+def test_misaligned_arrays_are_refused():
+    """int32 and fp32 arrays at multiples of 4 bytes, masks at multiples of 8: as the kernels load them."""
+    p = api.make_pages(**PAGES)
+    ok = dict(p=C.byref(p), pool=FAKE, table=FAKE, mp=4, lens=FAKE, batch=1, n=2, nq=8, counts=None, mask=None, q=FAKE,
+              qb=2048, qt=1024, k=FAKE, v=FAKE, kb=512, kt=256, scale=0.1, po=None, pl=None, out=FAKE, lse=None, ws=FAKE,
+              wsb=1 << 30)
+    for over in (dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(counts=FAKE + 2), dict(mask=FAKE + 4), dict(lse=FAKE + 2),
+                 dict(po=FAKE, pl=FAKE + 2), dict(po=FAKE + 1, pl=FAKE)):
+        assert _lib.lib().jolt_tree_attn(*(ok | over).values(), None) == BAD, over
+    ok = dict(p=C.byref(p), pool=FAKE, table=FAKE, mp=4, lens=FAKE, batch=1, n=2, counts=None, src=None, n_src=2, k=FAKE,
+              v=FAKE, sb=512, st=256, err=None)
+    for over in (dict(table=FAKE + 1), dict(lens=FAKE + 2), dict(counts=FAKE + 2), dict(src=FAKE + 2), dict(err=FAKE + 2)):
+        assert _lib.lib().jolt_pages_append(*(ok | over).values(), None) == BAD, over
+    ok = dict(p=C.byref(p), pool=FAKE, table=FAKE, mp=4, lens=FAKE, batch=1, start=None, n=2, k=FAKE, v=FAKE, sb=512,
+              sh=256, err=None)
+    for over in (dict(table=FAKE + 2), dict(lens=FAKE + 2), dict(start=FAKE + 2), dict(err=FAKE + 1)):
+        assert _lib.lib().jolt_pages_read(*(ok | over).values(), None) == BAD, over
+    ok = dict(q=FAKE, qo=FAKE, nq=4, sq=512, sqo=512, k=FAKE, ko=FAKE, nkv=2, sk=256, sko=256, n=3, d=128, rot=128,
+              layout=0, pos=FAKE, freq=FAKE, scaling=1.0, inverse=0, io=1)
+    for over in (dict(pos=FAKE + 2), dict(freq=FAKE + 2)):
+        assert _lib.lib().jolt_rope(*(ok | over).values(), None) == BAD, over
