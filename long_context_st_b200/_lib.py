@@ -48,6 +48,14 @@ class Pages(C.Structure):
     _fields_ = [("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_kv", C.c_int32), ("d_h", C.c_int32),
                 ("b_k", C.c_int32), ("b_v", C.c_int32), ("io_dtype", C.c_int32), ("rot_seed", C.c_uint64)]
 
+    def __setattr__(self, name, value):
+        if "_bytes" in self.__dict__ and name in _PAGES_FIELDS:  # the pool's size has been formed from them
+            raise AttributeError(f"{name}: pages are described once (make_pages)")
+        super().__setattr__(name, value)
+
+
+_PAGES_FIELDS = frozenset(name for name, _ in Pages._fields_)
+
 
 # (name, restype, argtypes) of every entry point declared in include/jolt.h
 _P = C.c_void_p

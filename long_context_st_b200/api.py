@@ -428,7 +428,8 @@ def _here(pages, pool, table, lens):
 
 
 def make_pages(n_pages, page_size, n_kv, d_h, b_k, b_v, io_dtype="bf16", rot_seed=0) -> Pages:
-    """Description of a tail cache's pages (jolt_pages); raises when the library cannot serve it."""
+    """Description of a tail cache's pages (jolt_pages), whose fields then stay as they are; raises when the
+    library cannot serve it."""
     p = Pages(n_pages, page_size, n_kv, d_h, b_k, b_v, _DT[io_dtype], rot_seed)
     p._bytes = int(lib().jolt_pages_bytes(C.byref(p)))
     if p._bytes == 0:

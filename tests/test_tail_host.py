@@ -238,3 +238,13 @@ def test_misaligned_arrays_are_refused():
               layout=0, pos=FAKE, freq=FAKE, scaling=1.0, inverse=0, io=1)
     for over in (dict(pos=FAKE + 2), dict(freq=FAKE + 2)):
         assert _lib.lib().jolt_rope(*(ok | over).values(), None) == BAD, over
+
+
+def test_a_description_of_pages_stays_as_it_was_made():
+    """The sizes that pools are checked against are formed once: a changed field would let a kernel past the pool."""
+    p = api.make_pages(**PAGES)
+    for field, value in (("n_pages", 400), ("page_size", 128), ("n_kv", 8), ("io_dtype", 0), ("b_v", 8)):
+        with pytest.raises(AttributeError):
+            setattr(p, field, value)
+    off, size = api.pages_layout(p)
+    assert api.pages_bytes(p) == 4 * size and p.n_pages == 4
