@@ -9,7 +9,7 @@ import torch
 import oracle
 from long_context_st_b200 import api
 from tail_ref import NP, rows, f64, make_table, i32, fill_random
-from tail_bounds import HALF, attention64, check64, ratios
+from tail_bounds import HALF, attention64, check64, coded_rows, ratios
 from test_gpu_tail import attn_case, run_attn
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,192 @@ def test_one_workspace_serves_every_smaller_call(cuda_ok):
         c = c[:2] + (t,) + c[3:]
         got, want = run_attn(c, ws=ws), run_attn(c)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---- many tiles a block -------------------------------------------------------------------------------
+# A batch with more (sequence, KV head) pairs than blocks that fit the GPU at once leaves every sequence one split, so a
+# block of the tcgen05 form goes through ceil(length / 128) tiles and a warp of the other through ceil(length / 256).
+
+def hold(c, tight=True, drops=()):
+    """Holds a call to its bounds, and sees that a reference without one of these tokens is told apart."""
+    p, pool, table, lens, q, k, v, mask, cnt, pre = c
+    counts = None if cnt is None else cnt.tolist()
+    got = run_attn(c)
+    check64(*got, attention64(p, pool, table, lens, q, k, v, mask, counts, prefix=pre), counts, tight)
+    for b, t in drops:
+        one = [None if x is None else x[b:b + 1] for x in (table, lens, q, k, v, mask, counts)]
+        ref = attention64(p, pool, *one, prefix=None if pre is None else [x[b:b + 1] for x in pre], drop=[(0, t)])
+        assert max(ratios(got[0][b:b + 1], got[1][b:b + 1], ref, one[-1])) > 1, (b, t)
+    return got
+
+
+@pytest.mark.parametrize("io,n", [("bf16", 1), ("bf16", 4), ("bf16", 5), ("bf16", 9), ("bf16", 17), ("bf16", 40), ("f32", 1),
+                                  ("f32", 4), ("f32", 5), ("f32", 9), ("f32", 17), ("f32", 40)])
+@pytest.mark.parametrize("d,bk,bv,ps", [(64, 2, 2, 16), (64, 4, 4, 128), (64, 8, 2, 32), (128, 8, 8, 64), (128, 4, 8, 16)])
+def test_many_tiles_a_block(cuda_ok, io, n, d, bk, bv, ps):
+    lens = [3000 - 149 * i for i in range(20)]
+    c = attn_case(n * 3 + bk, lens, n, 16, 16, d, bk, bv, ps, io, counts=[n - (i % 4 == 3) for i in range(20)])
+    hold(c, drops=[(0, 2999), (2, lens[2] - 1), (0, 127), (0, 1279), (1, 2303), (1, 0), (4, ps - 1)])  # of sequences that have rows
+
+
+@pytest.mark.parametrize("n", [1, 5, 9, 17, 40])
+@pytest.mark.parametrize("b", [2, 4, 8])
+def test_rising_scores_and_changing_value_scales_over_many_tiles(cuda_ok, n, b):
+    """Keys whose scales grow to eight times, so that references are raised again and again; values 64 times as
+    large from tile 5 to tile 9, so that the unit of the sums changes late and stays above what follows."""
+    lens = [2500 - 131 * i for i in range(20)]
+    c = attn_case(n + b, lens, n, 16, 16, 64, 8, b, 32, "bf16")
+    p, pool, table = c[:3]
+    off, size = api.pages_layout(p)
+    pages = pool.view(p.n_pages, size)
+    for s, length in enumerate(lens):
+        for i in range(-(-length // 32)):
+            t = i * 32 + torch.arange(32, device="cuda").float()
+            page = pages[int(table[s, i])]
+            for seg, f in ((1, 1 + 7 * t / 2500), (3, torch.where((t >= 640) & (t < 1280), 64.0, 1.0))):
+                sz = page[off[seg]:off[seg] + 16 * 32 * 4].view(torch.float16).view(16, 32, 2)
+                sz.copy_((sz.float() * f[None, :, None]).half())
+    hold(c, tight=False)
+
+
+@pytest.mark.parametrize("io,n", [("bf16", 1), ("bf16", 17), ("f32", 17)])
+def test_splits_of_two_long_sequences(cuda_ok, io, n):
+    c = attn_case(71, [5003, 3001], n, 16, 16, 64, 8, 8, 16, io, prefix=True)
+    # splits have 9 tiles of 128 tokens with tcgen05, 14 or 15 of 32 (f32: 28) otherwise
+    hold(c, drops=[(0, 5002), (1, 3000)] + [(0, k * 128 - 1) for k in (1, 9, 18, 27)] + [(0, k * 32) for k in (14, 15, 28, 56)])
+
+
+@pytest.mark.parametrize("io,n,batch", [("bf16", 17, 30), ("bf16", 17, 150), ("bf16", 2, 30), ("f32", 12, 150)])
+def test_equal_weights_count_every_token(cuda_ok, io, n, batch):
+    """q = 0: the log-sum-exp is the logarithm of the length and the output the values' mean."""
+    around = [0, 1, 2] + [k * 128 + x for k in (1, 2, 3, 4, 5, 8, 9, 12) for x in (-1, 0, 1)] + [31, 33, 1800]
+    lens = [around[i % len(around)] for i in range(batch)]
+    c = attn_case(73, lens, n, 2, 2, 64, 4, 4, 16, io, drafted=False)
+    c[4].zero_()
+    _, lse = hold(c)
+    for b, length in enumerate(lens):
+        if length:
+            assert float((lse[b].exp().double() - length).abs().max()) < 0.05
+
+
+def test_captured_tree_follows_lengths_and_counts(cuda_ok):
+    """bf16 of 20 rows: one graph over lengths that grow from nothing past many tiles, and counts that change."""
+    full = [2100, 900, 1500]
+    c = attn_case(75, full, 20, 4, 4, 64, 4, 4, 16, "bf16")
+    p, pool, table, _, q, k, v, mask, _, _ = c
+    ws = api.new_tree_workspace(p, 3, 20, 4, table.shape[1])
+    lens, cnt = i32([0, 0, 0]), i32([20, 20, 20])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        api.tree_attn(p, pool, table, lens, q, out, ws, k=k, v=v, mask=mask, counts=cnt, lse=lse)
+    for now, many in (([0, 0, 0], [20, 20, 20]), ([1, 900, 128], [20, 0, 3]), (full, [20, 19, 1]), ([129, 0, 1500], [1, 20, 20]),
+                      ([0, 0, 1], [0, 0, 5])):
+        lens.copy_(i32(now)), cnt.copy_(i32(many))
+        out.fill_(9), lse.fill_(9)
+        graph.replay()
+        check64(out, lse, attention64(p, pool, table, now, q, k, v, mask, many), many, tight=False)
+        for b, m in enumerate(many):
+            assert bool((out[b, m:] == 9).all()) and bool((lse[b, m:] == 9).all())
+    api.check_ws(ws)
+
+
+# ---- pages and lengths that are not there ---------------------------------------------------------------
+
+@pytest.mark.parametrize("io,n", [("f32", 2), ("bf16", 2), ("bf16", 9), ("bf16", 20)])
+@pytest.mark.parametrize("ps", [16, 64])
+def test_bad_pages_and_lengths_give_what_is_documented(cuda_ok, io, n, ps):
+    """Tokens of a page that the table does not name are invisible, a length below 0 holds nothing and one past the
+    table all that the table names; each is reported."""
+    c = attn_case(77, [1500, 333], n, 4, 2, 64, 4, 8, ps, io, extra=2)
+    p, pool, table, lens, q, k, v, mask, _, _ = c
+    ws = api.new_tree_workspace(p, 2, n, 4, table.shape[1])
+
+    def call(t, now, same):
+        out, lse = torch.full_like(q, 9.0), torch.full(q.shape[:3], 9.0, device="cuda")
+        api.tree_attn(p, pool, t, i32(now), q, out, ws, k=k, v=v, mask=mask, lse=lse)
+        with pytest.raises(api.JoltError) as e:
+            api.check_ws(ws)
+        assert e.value.status == -1
+        ws[:4] = 0
+        check64(out, lse, attention64(p, pool, t, same, q, k, v, mask), tight=False)
+
+    for bad in (p.n_pages, -1, 2 ** 31 - 1, -2 ** 31):
+        for entries in ([(0, 0)], [(0, 1)], [(0, 2), (0, 3)], [(1, 0), (0, 1400 // ps), (0, 1499 // ps)]):
+            t = table.clone()
+            for s, i in entries:
+                t[s, i] = bad
+            call(t, lens, lens)
+    most = table.shape[1] * ps
+    for now, same in (([-3, 333], [0, 333]), ([-2 ** 31, -1], [0, 0]), ([1500, 10 ** 6], [1500, most]),
+                      ([2 ** 31 - 1, most + 1], [most, most])):
+        call(table, now, same)
+
+
+# ---- many rows a warp -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("io,d,bk,bv,ps", [("bf16", 128, 8, 4, 64), ("f32", 64, 2, 8, 16), ("bf16", 64, 4, 2, 128)])
+def test_append_of_many_rows_is_the_codec_bit_for_bit(cuda_ok, io, d, bk, bv, ps):
+    """45000 rows of each kind, where a round of the grid takes 18944; rows that are not written among them."""
+    rng = np.random.default_rng(81)
+    n, nkv, lens, counts = 5000, 3, [13, 0, 900], [5000, 4999, 4001]
+    table, n_pages = make_table(rng, [a + n for a in lens], ps)
+    p = api.make_pages(n_pages, ps, nkv, d, bk, bv, io_dtype=io, rot_seed=7)
+    pool = api.new_pool(p)
+    pool.fill_(0xA5)
+    k, v = rows(rng, (3, n, nkv, d), io, True), rows(rng, (3, n, nkv, d), io)
+    bad = table.clone()
+    bad[1, 4000 // ps] = n_pages  # sequence 1 has no page there
+    err = i32([0])
+    api.pages_append(p, pool, bad, i32(lens), k, v, counts=i32(counts), err=err)
+    assert int(err) == -1
+    want = torch.full_like(pool, 0xA5).view(n_pages, -1)
+    off, _ = api.pages_layout(p)
+    for x, which, b in ((k, 0, bk), (v, 1, bv)):
+        codes, sz, e = api.quantize_pack(api.rotate_rows(x.float().view(-1, d).contiguous(), 7), b)
+        assert int(e) == 0
+        rb, first = d * b // 8, off[2 * which]
+        c = want[:, first:first + nkv * ps * rb].unflatten(-1, (nkv, ps, rb))
+        z = want[:, off[2 * which + 1]:off[2 * which + 1] + nkv * ps * 4].unflatten(-1, (nkv, ps, 4))
+        for s in range(3):
+            t = lens[s] + torch.arange(counts[s], device="cuda")
+            page = bad[s].long()[t // ps]
+            ok = page < n_pages
+            c[page[ok], :, (t % ps)[ok]] = codes.view(3, n, nkv, rb)[s, :counts[s]][ok]
+            z[page[ok], :, (t % ps)[ok]] = sz.view(torch.uint8).view(3, n, nkv, 4)[s, :counts[s]][ok]
+    assert torch.equal(pool, want.view(-1))
+
+
+@pytest.mark.parametrize("io,d,bk,bv,ps", [("bf16", 64, 4, 8, 16), ("bf16", 128, 2, 4, 64), ("f32", 64, 8, 2, 32)])
+def test_read_of_many_tiles(cuda_ok, io, d, bk, bv, ps):
+    """600 tokens of 40 sequences and 32 heads: one block a line, so a warp has five tiles of 16; a page that is not
+    there in its fourth."""
+    rng = np.random.default_rng(83)
+    B, nkv, n = 40, 32, 600
+    lens = [700 - 17 * (i % 30) for i in range(B)]
+    start = [(5 * i) % 47 for i in range(B)]
+    table, n_pages = make_table(rng, lens, ps)
+    p = api.make_pages(n_pages, ps, nkv, d, bk, bv, io_dtype=io, rot_seed=12)
+    pool = api.new_pool(p)
+    fill_random(rng, p, pool)
+    gone = 450 // ps
+    table[3, gone] = -1
+    k_out, v_out = (torch.full((B, nkv, n, d), 7.0, dtype=NP[io], device="cuda") for _ in range(2))
+    err = i32([0])
+    api.pages_read(p, pool, table, i32(lens), k_out, v_out, start=i32(start), err=err)
+    assert int(err) == -1
+    R = torch.from_numpy(oracle.rotation_matrix(d, 12)).cuda()
+    for b in range(B):
+        m = min(n, lens[b] - start[b])
+        for o, (c, s, z) in zip((k_out, v_out), coded_rows(p, pool, table, b, lens[b])):
+            y = (c * s[..., None] + z[..., None])[:, start[b]:start[b] + m]
+            there = torch.isfinite(y[0, :, 0])
+            x = y[:, there] @ R
+            got = o[b, :, :m].double()
+            # a dequantised value is rounded once, the rotation adds d of them in log2(d) fp32 roundings
+            size = float(y[:, there].abs().max()) * math.sqrt(d)
+            assert float(((got[:, there] - x).abs() - HALF[NP[io]] * x.abs()).max()) <= (math.log2(d) + 3) * 2.0 ** -24 * size
+            assert bool((got[:, ~there] == 7).all()) and bool((o[b, :, m:] == 7).all())
+            assert bool(there.all()) == (b != 3)
