@@ -568,7 +568,11 @@ typedef enum {
   JOLT_K_DECODE_AUX = 3,    /* decode prologue, softmax, value residual, finalize, split merge */
   JOLT_K_CHOL = 4,          /* fp64 Cholesky + triangular inverse (CholeskyQR) */
   JOLT_K_EIG = 5,           /* fp64 block-Jacobi symmetric eigensolver */
-  JOLT_K_COUNT = 6
+  JOLT_K_ROPE = 6,          /* rotary positions */
+  JOLT_K_PAGES = 7,         /* tail cache rows written or read back; bytes as the call's sizes name them (lengths
+                               and counts are on the device) */
+  JOLT_K_TREE = 8,          /* attention over the tail cache, its merge included; work unknown to the host: 0 */
+  JOLT_K_COUNT = 9
 } jolt_kernel_family;
 
 typedef struct {

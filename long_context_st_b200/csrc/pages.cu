@@ -4,6 +4,7 @@
 #include "common.cuh"
 #include "pages_codes.cuh"
 #include "pages.cuh"
+#include "stats.h"
 
 namespace jolt {
 namespace {
@@ -492,6 +493,11 @@ bool pool_args_ok(const jolt_pages* p, const void* pool, const int32_t* table, i
   if (batch == 0) return true;
   return pool && table && lens && aligned(pool, 16) && aligned(table, 4) && aligned(lens, 4);
 }
+// Bytes of a K row, of a V row, or of both: coded, and as given.
+double row_bytes(const jolt_pages& p, bool k, bool v) {
+  const double plain = double(p.d_h) * dtype_bytes(p.io_dtype) + 4;
+  return (k ? p.d_h * p.b_k / 8 + plain : 0.0) + (v ? p.d_h * p.b_v / 8 + plain : 0.0);
+}
 bool rows_ok(const void* x, int64_t s0, int64_t s1) {
   return reinterpret_cast<uintptr_t>(x) % 16 == 0 && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
 }
@@ -528,6 +534,7 @@ extern "C" jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(unsigned(std::min<int64_t>((rows + kWarps * 8 - 1) / (kWarps * 8), 148 * 2)), 2);
   const bool f32 = pages->io_dtype == JOLT_F32;
+  StatScope sc(JOLT_K_PAGES, st, 0.0, double(rows) * row_bytes(*pages, true, true));
   if (pages->d_h == 128) {
     if (f32) k_append<float, 128><<<grid, kThreads, 0, st>>>(a);
     else k_append<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(a);
@@ -571,6 +578,7 @@ extern "C" jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool
   const int64_t most = std::max<int64_t>(1, (148 * 8 + lines - 1) / lines);
   const dim3 grid(unsigned(std::min((tiles + kWarps - 1) / kWarps, most)), 2 * pages->n_kv, batch);
   const bool f32 = pages->io_dtype == JOLT_F32;
+  StatScope sc(JOLT_K_PAGES, st, 0.0, double(batch) * n_out * pages->n_kv * row_bytes(*pages, k_out, v_out));
   if (pages->d_h == 128) {
     if (f32) k_read<float, 128><<<grid, kThreads, 0, st>>>(a);
     else k_read<__nv_bfloat16, 128><<<grid, kThreads, 0, st>>>(a);

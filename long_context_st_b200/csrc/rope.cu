@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "stats.h"
 
 namespace jolt {
 namespace {
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(const RopeArgs a) {
 template <typename T>
 jolt_status launch_rope(RopeArgs a, bool half, bool vec, cudaStream_t st) {
   const int heads = a.t[0].heads + a.t[1].heads, pairs = a.rot / 2;
+  const double bytes = double(a.n_tokens) * (2.0 * heads * a.d * sizeof(T) + 4.0);
   if (vec) {
     constexpr int V = 16 / sizeof(T);
     const int units = (half ? pairs : a.rot) / V + (a.d - a.rot) / V, at_once = kThreads / units;
@@ -204,11 +206,13 @@ jolt_status launch_rope(RopeArgs a, bool half, bool vec, cudaStream_t st) {
     const int64_t total = a.n_tokens * heads, grid = (total + rows - 1) / rows;
     if (grid > 0x7fffffff) return JOLT_ERR_INVALID_ARG;
     const size_t smem = size_t(std::min<int64_t>(rows / heads + 2, a.n_tokens)) * pairs * sizeof(float2);
+    StatScope sc(JOLT_K_ROPE, st, 0.0, bytes);
     if (half) k_rope_vec<T, true><<<unsigned(grid), kThreads, smem, st>>>(a);
     else k_rope_vec<T, false><<<unsigned(grid), kThreads, smem, st>>>(a);
   } else {
     const unsigned grid = unsigned((a.n_tokens + a.tb - 1) / a.tb);
     const size_t smem = size_t(a.tb) * pairs * sizeof(float2);
+    StatScope sc(JOLT_K_ROPE, st, 0.0, bytes);
     if (half) k_rope_any<T, true><<<grid, kThreads, smem, st>>>(a);
     else k_rope_any<T, false><<<grid, kThreads, smem, st>>>(a);
   }

@@ -23,6 +23,7 @@
 
 #include "pages_codes.cuh"
 #include "sm100.cuh"
+#include "stats.h"
 #include "tree_attn.cuh"
 
 namespace jolt {
@@ -794,6 +795,7 @@ extern "C" jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool,
   a.stage_bytes = t.stage_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f32 = pages->io_dtype == JOLT_F32;
+  StatScope sc(JOLT_K_TREE, st, 0.0, 0.0);
   if (pages->d_h == 128)
     return f32 ? launch_tree_d<float, 128>(a, t, k != nullptr, st) : launch_tree_d<__nv_bfloat16, 128>(a, t, k != nullptr, st);
   return f32 ? launch_tree_d<float, 64>(a, t, k != nullptr, st) : launch_tree_d<__nv_bfloat16, 64>(a, t, k != nullptr, st);

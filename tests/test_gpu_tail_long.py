@@ -249,3 +249,26 @@ def test_read_of_many_tiles(cuda_ok, io, d, bk, bv, ps):
             assert float(((got[:, there] - x).abs() - HALF[NP[io]] * x.abs()).max()) <= (math.log2(d) + 3) * 2.0 ** -24 * size
             assert bool((got[:, ~there] == 7).all()) and bool((o[b, :, m:] == 7).all())
             assert bool(there.all()) == (b != 3)
+
+
+def test_kernel_timing_sees_the_tail_caches_calls(cuda_ok):
+    c = attn_case(91, [100, 30], 3, 4, 2, 64, 4, 8, 16, "bf16")
+    p, pool, table, lens, q, k, v = c[:7]
+    back = torch.empty(2, 2, 100, 64, dtype=torch.bfloat16, device="cuda")
+    pos, freq = i32([0, 1, 2]), torch.ones(32, device="cuda")
+    api.stats_read(reset=True)
+    api.stats_enable(True)
+    try:
+        api.rope(q[0], k[0], pos, freq)
+        run_attn(c)
+        api.pages_read(p, pool, table, i32(lens), back, back.clone())
+        api.pages_read(p, pool, table, i32(lens), back, None)
+        api.pages_append(p, pool, table, i32([0, 0]), k, v)
+    finally:
+        api.stats_enable(False)
+    s = api.stats_read(reset=True)
+    assert (s["rope"]["launches"], s["pages"]["launches"], s["tree"]["launches"]) == (1, 3, 1)
+    assert all(s[f]["ms"] > 0 for f in ("rope", "pages", "tree"))
+    assert s["rope"]["bytes"] == 3 * (2 * 6 * 64 * 2 + 4)
+    k_row, v_row = 64 * 4 // 8 + 4 + 64 * 2, 64 * 8 // 8 + 4 + 64 * 2
+    assert s["pages"]["bytes"] == 2 * 2 * (100 * (k_row + v_row) + 100 * k_row + 3 * (k_row + v_row))

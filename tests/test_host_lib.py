@@ -261,3 +261,10 @@ def test_noalloc_decode_checks_arguments_before_scratch_size():
     assert r_big == -6
     r_pos = lib().jolt_decode_attn_noalloc(C.byref(s), good, fake, 0, w.n_layers, fake, fake, None, inv, -1, None)
     assert r_pos == -1
+
+
+def test_kernel_families_are_the_headers():
+    txt = open(os.path.join(ROOT, "include", "jolt.h")).read()
+    names = re.findall(r"\bJOLT_K_([A-Z_]+) = (\d+)", txt)
+    assert [n.lower() for n, _ in names[:-1]] == _lib.KERNEL_FAMILIES
+    assert names[-1] == ("COUNT", str(len(_lib.KERNEL_FAMILIES)))
