@@ -493,7 +493,11 @@ def pages_read(p: Pages, pool, table, lens, k_out=None, v_out=None, start=None, 
 
 def tree_mask(parents):
     """Ancestor masks uint64 [n] of a drafted tree: parents[i] < i, or -1 for a root."""
-    a = np.ascontiguousarray(parents, dtype=np.int32)
+    given = np.asarray(parents)
+    with np.errstate(invalid="ignore"):
+        a = np.ascontiguousarray(given).astype(np.int32) if given.size else np.zeros(0, dtype=np.int32)
+    if given.ndim != 1 or not np.array_equal(a, given):
+        _bad("parents: a list of whole numbers is wanted")
     out = np.zeros(a.size, dtype=np.uint64)
     check(lib().jolt_tree_mask(a.ctypes.data, a.size, out.ctypes.data), "jolt_tree_mask")
     return out

@@ -248,3 +248,12 @@ def test_a_description_of_pages_stays_as_it_was_made():
             setattr(p, field, value)
     off, size = api.pages_layout(p)
     assert api.pages_bytes(p) == 4 * size and p.n_pages == 4
+
+
+def test_tree_mask_takes_whole_numbers_alone():
+    """A parent that int32 or whole numbers cannot hold is refused, not cut to one that they can."""
+    for bad in (np.array([-1, 2 ** 32]), np.array([2 ** 32 - 1]), [-1, 0.5], np.array([-1.5]), [[-1, 0]], [-1, math.nan]):
+        with pytest.raises(api.JoltError):
+            api.tree_mask(bad)
+    for good in (np.array([-1, 0], dtype=np.int64), [-1.0, 0.0], (-1, 0)):
+        assert api.tree_mask(good).tolist() == [1, 3]
