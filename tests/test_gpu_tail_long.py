@@ -272,3 +272,61 @@ def test_kernel_timing_sees_the_tail_caches_calls(cuda_ok):
     assert s["rope"]["bytes"] == 3 * (2 * 6 * 64 * 2 + 4)
     k_row, v_row = 64 * 4 // 8 + 4 + 64 * 2, 64 * 8 // 8 + 4 + 64 * 2
     assert s["pages"]["bytes"] == 2 * 2 * (100 * (k_row + v_row) + 100 * k_row + 3 * (k_row + v_row))
+
+
+# ---- what one row or caller does to the others ------------------------------------------------------------
+
+@pytest.mark.parametrize("io,n", [("f32", 3), ("bf16", 3), ("bf16", 7), ("bf16", 12), ("f32", 20), ("bf16", 20), ("bf16", 40)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_that_is_not_finite_stays_on_its_own(cuda_ok, io, n, bad):
+    c = attn_case(93, [700, 40], n, 4, 4, 128, 4, 4, 32, io, prefix=True)
+    p, pool, table, lens, q, k, v, mask, cnt, pre = c
+    ref = attention64(p, pool, table, lens, q, k, v, mask, prefix=pre)
+    rows_ = ((0, n // 2, 1, 5), (0, 0, 2, 0), (1, n - 1, 0, 127))
+    for b, i, h, e in rows_:
+        q[b, i, h, e] = bad
+    out, lse = run_attn(c)
+    for b, i, h, _ in rows_:
+        assert bool(out[b, i, h].isnan().all()) and not math.isfinite(float(lse[b, i, h]))
+        out[b, i, h], lse[b, i, h] = ref[0][b, i, h].to(out.dtype), ref[1][b, i, h].float()
+    check64(out, lse, ref, tight=False)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_broadcast_inputs(cuda_ok, n):
+    """One set of queries and drafted rows for all sequences (stride 0)."""
+    c = attn_case(95, [300, 0, 77], n, 8, 4, 64, 4, 4, 16, "bf16")
+    p, pool, table, lens, q, k, v, mask, _, _ = c
+    q1, k1, v1, m1 = (x[:1].expand(3, *x.shape[1:]) for x in (q, k, v, mask))
+    want = run_attn(c[:4] + (q1.contiguous(), k1.contiguous(), v1.contiguous(), m1.contiguous(), None, None))
+    ws = api.new_tree_workspace(p, 3, n, 8, table.shape[1])
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    api.tree_attn(p, pool, table, i32(lens), q1, out, ws, k=k1, v=v1, mask=m1.contiguous(), lse=lse)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(api.JoltError):
+        api.tree_attn(p, pool, table, i32(lens), q1, out, ws, k=k1, v=v1, mask=m1, lse=lse)
+
+
+def test_calls_at_once_of_both_forms_repeat_bit_for_bit(cuda_ok):
+    """Trees of both forms, and a read, on four streams, over and over, with workspaces of their own."""
+    cs = [attn_case(96 + i, [2000 + 300 * i, 500], n, 8, 4, 128, 4, 4, 64, io)
+          for i, (n, io) in enumerate(((20, "bf16"), (20, "bf16"), (1, "bf16"), (9, "f32")))]
+    want = [run_attn(c) for c in cs]
+    p, pool, table, lens = cs[0][:4]
+    back = torch.empty(2, 4, 1500, 128, dtype=torch.bfloat16, device="cuda")
+    api.pages_read(p, pool, table, i32(lens), back, None)
+    want_back = back.clone()
+    streams = [torch.cuda.Stream() for _ in cs]
+    bufs = [(torch.empty_like(w[0]), torch.empty_like(w[1])) for w in want]
+    wss = [api.new_tree_workspace(c[0], 2, c[4].shape[1], 8, c[2].shape[1]) for c in cs]
+    ls = [i32(c[3]) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, s, b, ws, l in zip(cs, streams, bufs, wss, ls):
+            api.tree_attn(c[0], c[1], c[2], l, c[4], b[0], ws, k=c[5], v=c[6], mask=c[7], lse=b[1], stream=s.cuda_stream)
+        api.pages_read(p, pool, table, ls[0], back, None, stream=streams[0].cuda_stream)
+    torch.cuda.synchronize()
+    for b, w, ws in zip(bufs, want, wss):
+        api.check_ws(ws)
+        assert torch.equal(b[0], w[0]) and torch.equal(b[1], w[1])
+    assert torch.equal(back[:, :, :500], want_back[:, :, :500])
