@@ -5,40 +5,13 @@
 #include "pages_codes.cuh"
 #include "pages.cuh"
 #include "stats.h"
+#include "vec.cuh"
 
 namespace jolt {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-
-// Two fp32 values in one 64-bit register, added or multiplied in one instruction each (IEEE per half).
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 f2_make(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_get(f2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // Both kernels hold a row of D elements in four lanes, eight rows a warp (or sixteen as MMA rows): lane
 // m = lane % 4 has the 8-element pieces j*4 + m, j < D/32, so a load or store of one piece a lane covers
@@ -82,18 +55,7 @@ struct Raw8 {
   }
   __device__ __forceinline__ void floats(float* f) const {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          f[4 * i + e] = __uint_as_float(w[e]);
-        } else {
-          f[2 * e] = __uint_as_float(w[e] << 16);
-          f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
-      }
-    }
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) unpack16<T>(v[i], f + 16 / int(sizeof(T)) * i);
   }
 };
 
@@ -318,24 +280,6 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int m, uint32_t (
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Sixteen rows (16 aligned tokens of one head, so of one page) a warp. With the codes centred,
 //   H (scale c + zero) = scale (H c') + (D (zero + o scale)) e_0,   o = 2^(b-1),
 // so the Hadamard transform runs on whole numbers, exactly: four of the feature index's bits (those of
@@ -407,7 +351,9 @@ __device__ __forceinline__ void read_tile(const uint32_t (&w)[2][D * B / 128], c
         v[e] = __uint_as_float(__float_as_uint(x.x) ^ ((neg << (31 - 8 * j - e)) & 0x80000000u));
         v[e + 1] = __uint_as_float(__float_as_uint(x.y) ^ ((neg << (30 - 8 * j - e)) & 0x80000000u));
       }
-      store8<T>(dst + piece_at(j, m), v);
+#pragma unroll
+      for (int i = 0; i < int(sizeof(T)) / 2; ++i)
+        reinterpret_cast<uint4*>(dst + piece_at(j, m))[i] = pack16<T>(v + 16 / int(sizeof(T)) * i);
     }
   }
 }
@@ -498,10 +444,6 @@ double row_bytes(const jolt_pages& p, bool k, bool v) {
   const double plain = double(p.d_h) * dtype_bytes(p.io_dtype) + 4;
   return (k ? p.d_h * p.b_k / 8 + plain : 0.0) + (v ? p.d_h * p.b_v / 8 + plain : 0.0);
 }
-bool rows_ok(const void* x, int64_t s0, int64_t s1) {
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
-}
-
 }  // namespace
 }  // namespace jolt
 
@@ -532,7 +474,7 @@ extern "C" jolt_status jolt_pages_append(const jolt_pages* pages, void* pool, co
   a.n_new = n_new;
   a.n_src = n_src;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(unsigned(std::min<int64_t>((rows + kWarps * 8 - 1) / (kWarps * 8), 148 * 2)), 2);
+  const dim3 grid(unsigned(std::min<int64_t>((rows + kWarps * 8 - 1) / (kWarps * 8), kSmCount * 2)), 2);
   const bool f32 = pages->io_dtype == JOLT_F32;
   StatScope sc(JOLT_K_PAGES, st, 0.0, double(rows) * row_bytes(*pages, true, true));
   if (pages->d_h == 128) {
@@ -575,7 +517,7 @@ extern "C" jolt_status jolt_pages_read(const jolt_pages* pages, const void* pool
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // tiles of 16 aligned tokens that n_out rows can touch, and warps for them until the GPU is full
   const int64_t tiles = (int64_t(n_out) + 30) / 16, lines = int64_t(batch) * pages->n_kv * 2;
-  const int64_t most = std::max<int64_t>(1, (148 * 8 + lines - 1) / lines);
+  const int64_t most = std::max<int64_t>(1, (kSmCount * 8 + lines - 1) / lines);
   const dim3 grid(unsigned(std::min((tiles + kWarps - 1) / kWarps, most)), 2 * pages->n_kv, batch);
   const bool f32 = pages->io_dtype == JOLT_F32;
   StatScope sc(JOLT_K_PAGES, st, 0.0, double(batch) * n_out * pages->n_kv * row_bytes(*pages, k_out, v_out));

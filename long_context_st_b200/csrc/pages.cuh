@@ -9,6 +9,11 @@ namespace jolt {
 bool pages_ok(const jolt_pages* p);
 inline bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }  // NULL is
 
+// Rows of K, V or q with these element strides can be loaded 16 bytes at a time.
+inline bool rows_ok(const void* x, int64_t s0, int64_t s1) {
+  return aligned(x, 16) && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
+}
+
 // Byte offsets of a page's segments and its size.
 struct PageLayout {
   uint32_t kc, ks, vc, vs;

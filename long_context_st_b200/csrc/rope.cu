@@ -3,6 +3,7 @@
 
 #include "common.cuh"
 #include "stats.h"
+#include "vec.cuh"
 
 namespace jolt {
 namespace {
@@ -42,40 +43,6 @@ __device__ __forceinline__ void rope_table(const RopeArgs& a, int64_t t0, int nt
   __syncthreads();
 }
 
-template <typename T>
-struct Vec {  // 16 bytes
-  static constexpr int N = 16 / sizeof(T);
-  uint4 raw;
-};
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& r, float (&f)[Vec<T>::N]) {
-  if constexpr (sizeof(T) == 4) {
-    f[0] = __uint_as_float(r.x); f[1] = __uint_as_float(r.y);
-    f[2] = __uint_as_float(r.z); f[3] = __uint_as_float(r.w);
-  } else {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::N]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      w[i] = __float_as_uint(f[i]);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Bound by HBM: every element is read and written once. Four rows of loads in flight a thread: 8192 tokens of
 // 64 + 8 heads of 128 in bf16 take 59.6 us (302 MB, 5.1 TB/s), 5003 tokens of 32 + 8 heads in fp32 34.9 us
 // (205 MB, 5.9 TB/s). What bf16 lacks to the copy rate is latency: the table (double precision, once a block) and
@@ -89,7 +56,7 @@ __device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::N]) {
 constexpr int kRows = 4;
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
-  constexpr int V = Vec<T>::N;
+  constexpr int V = 16 / sizeof(T);
   extern __shared__ float2 cs[];
   const int half = a.rot >> 1;
   const int rot_units = HALF ? half / V : a.rot / V;
@@ -134,17 +101,17 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
     }
     const float2* c = cs + tok[i] * half;
     float p[V], y[V];
-    unpack<T>(pa[i], p);
+    unpack16<T>(pa[i], p);
     if (HALF) {
       float q[V], z[V];
-      unpack<T>(pb[i], q);
+      unpack16<T>(pb[i], q);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float2 f = c[u * V + j];
         y[j] = p[j] * f.x - q[j] * f.y;
         z[j] = q[j] * f.x + p[j] * f.y;
       }
-      *reinterpret_cast<uint4*>(dst[i] + half) = pack<T>(z);
+      *reinterpret_cast<uint4*>(dst[i] + half) = pack16<T>(z);
     } else {
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
@@ -153,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_vec(const RopeArgs a) {
         y[2 * j + 1] = p[2 * j + 1] * f.x + p[2 * j] * f.y;
       }
     }
-    *reinterpret_cast<uint4*>(dst[i]) = pack<T>(y);
+    *reinterpret_cast<uint4*>(dst[i]) = pack16<T>(y);
   }
 }
 
@@ -260,7 +227,7 @@ extern "C" jolt_status jolt_rope(const void* q, void* q_out, int32_t n_q, int64_
   a.rot = rot_dim;
   a.inverse = inverse;
   // several tokens a block once there are blocks enough for every SM
-  a.tb = int(std::min<int64_t>(4, std::max<int64_t>(1, n_tokens / (148 * 8))));
+  a.tb = int(std::min<int64_t>(4, std::max<int64_t>(1, n_tokens / (kSmCount * 8))));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return io_dtype == JOLT_F32 ? launch_rope<float>(a, layout == JOLT_ROPE_HALF, vec, st)
                               : launch_rope<__nv_bfloat16>(a, layout == JOLT_ROPE_HALF, vec, st);

@@ -25,6 +25,7 @@
 #include "sm100.cuh"
 #include "stats.h"
 #include "tree_attn.cuh"
+#include "vec.cuh"
 
 namespace jolt {
 namespace {
@@ -657,7 +658,7 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
     t.smem = std::max(head + std::max(ring, red), draft);
   }
   // one block an SM for each 128 rows, or two where the registers allow: as many shares as are resident at once
-  const int heads = p.n_kv * t.blocks, resident = 148 * (!t.tc && t.nt == 1 ? 2 : 1);
+  const int heads = p.n_kv * t.blocks, resident = kSmCount * (!t.tc && t.nt == 1 ? 2 : 1);
   const int64_t tile = t.tc ? 128 : kTile;
   const int64_t tiles = (int64_t(max_pages) * p.page_size + tile - 1) / tile;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, (tiles + t.least - 1) / t.least));
@@ -713,10 +714,6 @@ jolt_status launch_tree_d(const TreeArgs& a, const TreePlan& t, bool draft, cuda
   if (t.nt == 2) return launch_tree<T, D, 2, false>(a, t, draft, st);
   if constexpr (sizeof(T) == 4) return launch_tree<T, D, 4, false>(a, t, draft, st);
   return JOLT_ERR_INVALID_ARG;  // bf16 of more than 16 rows is t.tc
-}
-
-bool rows_ok(const void* x, int64_t s0, int64_t s1) {
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && s0 >= 0 && s1 >= 0 && s0 % 8 == 0 && s1 % 8 == 0;
 }
 
 }  // namespace

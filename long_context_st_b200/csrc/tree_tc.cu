@@ -27,6 +27,7 @@
 #include "pages_codes.cuh"
 #include "sm100.cuh"
 #include "tree_attn.cuh"
+#include "vec.cuh"
 
 namespace jolt {
 namespace {
@@ -89,32 +90,6 @@ __device__ __forceinline__ uint32_t idesc_f16(int N, int b_mn_major) {
   return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
 
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 f2_make(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_get(f2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // 16 lanes x 32 columns of tensor memory: register 4a + {0, 1} = (lane g, columns 8a + 2m, +1), + {2, 3} the
 // same of lane g + 8.
 __device__ __forceinline__ void ld_16x256(uint32_t t, uint32_t (&r)[16]) {
