@@ -500,10 +500,14 @@ size_t jolt_tree_attn_workspace(const jolt_pages* pages, int32_t batch, int32_t 
  *            first call (the error word, read by jolt_check); calls sharing a ws must not overlap in time
  * Scores and softmax statistics are fp32. bf16 with more than 16 query rows (n_new * n_q / n_kv) runs its
  * products on tcgen05, the rest on m16n8k16 MMAs. What goes into the products in fewer bits than fp32's 24: R q in 22;
- * the weights in 11 for bf16 (22 for fp32; 16 over the drafted tokens' values), with tcgen05 the values in 11 too.
+ * the weights in 11 for bf16 (22 for fp32; 16 over the drafted tokens' values), with tcgen05 the values in 11 too;
+ * bf16's sums over keys of 4 and 8 bits keep 18 and 22 (log-sum-exps within some 1e-5 all the same).
  * So a bf16 output is off by its own rounding (2^-9 of a row's norm in the mean) and some 2^-11 of the root of the
  * summed squares of weight times value. A value row some 2^15 times the others (2^13 where fp32 tensors' 22 bits
- * count) costs them bits, whatever its weight. Asynchronous on `stream`. */
+ * count) costs them bits, whatever its weight.
+ * The work is divided evenly over the GPU for a batch well below 296 / n_kv sequences (up to 8 query rows a KV head;
+ * 148 / n_kv up to 16, beyond that for every 128 in bf16 and every 32 in fp32); from there on a sequence's KV head is
+ * one block's work, and the longest sequence sets the time. Asynchronous on `stream`. */
 jolt_status jolt_tree_attn(const jolt_pages* pages, const void* pool, const int32_t* table, int32_t max_pages,
                            const int32_t* lens, int32_t batch, int32_t n_new, int32_t n_q, const int32_t* counts,
                            const uint64_t* mask, const void* q, int64_t q_stride_b, int64_t q_stride_t,

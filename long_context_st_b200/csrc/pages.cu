@@ -106,7 +106,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // product leaves (-1/2, levels + 1/2) and has to be clipped (the extremes' products tell), takes the
 // division for all of its rows; on Gaussian rows that is one warp in 70 at 4 bits, one in 5 at 8.
 // Four lanes a row keep two of the seven butterfly stages between lanes; the others are packed adds in registers,
-// and the next rows' loads are in flight meanwhile. Bound by issue, some 108 instructions a row: 8191 tokens of 8
+// and the next rows' loads are in flight meanwhile. Bound by latency, 108 instructions a row in chains that 16 warps an SM
+// do not cover, and by a grid whose last round is part empty (K and V rows in blocks of their own): 8191 tokens of 8
 // heads at 8 and 4 bits take 27.5 us (46 MB; 1.7 TB/s, issue slots 54% busy at 128 registers, two blocks an SM).
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2) k_append(const AppendArgs a) {
@@ -285,7 +286,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int m, uint32_t (
 // so the Hadamard transform runs on whole numbers, exactly: four of the feature index's bits (those of
 // a pair's place among the k-slots of one m16n8k16 step) by MMAs with a matrix of signs, the others (the
 // step's) by butterflies of the accumulators. One rounding for scale / sqrt(D), one product, one
-// rounding to the output's type. Bound by the writes and, within 30% of them, by issue (32 instructions a row):
+// rounding to the output's type. Bound by latency at 16 warps an SM (32 instructions a row; a store covers 64 bytes of
+// one), at 72% of the copy rate:
 // 65536 tokens of 8 heads at 4 bits into bf16 take 71.9 us (340 MB, 4.7 TB/s, issue slots 48% busy).
 template <typename T, int D, int B>
 __device__ __forceinline__ void read_tile(const uint32_t (&w)[2][D * B / 128], const __half2 (&szs)[2], int g, int m, float isd,

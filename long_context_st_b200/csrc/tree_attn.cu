@@ -113,9 +113,9 @@ __device__ __forceinline__ void values_tile(const uint8_t* vc, const uint32_t (&
 // PACK (at most 4 rows) columns 0-3 carry the first term of R q and 4-7 the second, and the values
 // the two terms of p likewise. Each warp takes 32-token tiles of its own through a ring of bulk
 // copies (one mbarrier a stage); the warps meet at the end, to add up their partial results.
-// Bound by issue, some 385 instructions for 16 tokens of both kinds at 4 bits (codes to operands, MMAs that fill 4
-// of 8 columns, one softmax over 32 tokens at a time), and by some 10 us of launch, first loads and merge: one token
-// of four sequences of 64K to 40K, 8 KV heads, takes 65.7 us with the merge (232 MB, 3.5 TB/s; each further token
+// Bound by latency: some 385 instructions for 16 tokens of both kinds at 4 bits (codes to operands, MMAs that fill 4
+// of 8 columns, one softmax over 32 tokens at a time) are one chain a warp, four warps a scheduler; and by some
+// 10 us of launch, first loads and merge. One token of four sequences of 64K to 40K, 8 KV heads, takes 65.7 us with the merge (232 MB, 3.5 TB/s; each further token
 // costs what 4.4 TB/s would), issue slots 60% busy at two blocks of 126 registers an SM.
 template <typename T, int D, int NT, bool PACK>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_tree(const TreeArgs a) {
@@ -657,7 +657,11 @@ TreePlan tree_plan(const jolt_pages& p, int batch, int n_new, int n_q, int max_p
     const size_t draft = draft_smem(p.d_h, t.pack ? 4 : C, kThreads);
     t.smem = std::max(head + std::max(ring, red), draft);
   }
-  // one block an SM for each 128 rows, or two where the registers allow: as many shares as are resident at once
+  // As many shares as are resident at once: one block an SM, or two where the registers allow (at 8 bits of both kinds
+  // and d_h 128 the ring leaves room for one, and the shares run in two rounds: four tokens over 64K each take 118
+  // us against 78 at 4 bits, on 1.9 times the bytes). A batch with more (sequence, KV head) pairs than that, or as
+  // many, leaves a pair one block, and the longest sequence sets the time: 8 KV heads, one token, one sequence of 64K and 15
+  // of 2K take 41 us (four equal ones of as many tokens in all: 38), with 36 of 2K 376 (48).
   const int heads = p.n_kv * t.blocks, resident = kSmCount * (!t.tc && t.nt == 1 ? 2 : 1);
   const int64_t tile = t.tc ? 128 : kTile;
   const int64_t tiles = (int64_t(max_pages) * p.page_size + tile - 1) / tile;

@@ -61,7 +61,8 @@ __device__ __forceinline__ int64_t out_row(const TreeArgs& a, int b, int h, int 
   return (int64_t(b) * a.n_new + t) * a.n_q + h * a.gq + (row - t * a.gq);
 }
 // ---- how the pages' tokens are divided ----
-// A (KV head, row block) has `shares` blocks for the tiles of all sequences. Balanced: a split has c tiles, the
+// A (KV head, row block) has `shares` blocks for the tiles of all sequences (tree_plan says how many; where they
+// only equal the sequences in number, each gets one split). Balanced: a split has c tiles, the
 // least c (of a few) for which all sequences' splits number at most `shares`, so a ragged batch keeps every
 // block equally long (lengths 64K, 56K, 48K, 40K: 23% over a division of each sequence by the same number).
 // The lengths are on the device, so a warp works this out for itself; lane i has sequences 4 i .. + 3.

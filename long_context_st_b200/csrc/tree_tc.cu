@@ -16,10 +16,11 @@
 // Features stand in the order in which the widening leaves them; R q is laid out to match, and the merge puts
 // the outputs back.
 //
-// 256 query rows over 131072 tokens, 8 KV heads: 190 us with the merge, 0.72 PFLOP/s of the two products (the keys'
-// second term makes it 1.1 of MMA work; tensor pipe 48% busy). The roles alone take 115 us (MMAs, whose operands
-// share the shared memory with the widening's stores), 93 (softmax) and as much (widening); together they wait for
-// one another at a tile's end. Each block of 128 rows widens the codes for itself.
+// 256 query rows over 131072 tokens, 8 KV heads: 198 us with the merge in a run of graph replays, 208 with L2 flushed
+// between them; 0.69 and 0.66 PFLOP/s of the two products (the keys' second term makes it half as much again of MMA
+// work; tensor pipe 48% busy). The roles alone take 115 us (MMAs, whose operands share the shared memory with
+// the widening's stores), 93 (softmax) and as much (widening); together they wait for one another at a tile's end, with
+// two buffers a kind. Each block of 128 rows widens the codes for itself, and a block of fewer rows takes as long.
 #include <cuda.h>
 
 #include <algorithm>
