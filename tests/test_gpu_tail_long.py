@@ -330,3 +330,79 @@ def test_calls_at_once_of_both_forms_repeat_bit_for_bit(cuda_ok):
         api.check_ws(ws)
         assert torch.equal(b[0], w[0]) and torch.equal(b[1], w[1])
     assert torch.equal(back[:, :, :500], want_back[:, :, :500])
+
+
+# ---- offsets past 32 bits -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("io,n", [("bf16", 2), ("bf16", 20), ("f32", 9)])
+def test_a_pool_past_four_gigabytes(cuda_ok, io, n):
+    """The same pages at the end of a 5.4 GB pool and in one of their own: written, attended to and read back alike."""
+    rng = np.random.default_rng(97)
+    lens, new, nkv, d, ps = [900, 130], 40, 8, 128, 128
+    table, few = make_table(rng, [x + new for x in lens], ps)
+    small = api.make_pages(few, ps, nkv, d, 8, 8, io_dtype=io, rot_seed=5)
+    big = api.make_pages(20000, ps, nkv, d, 8, 8, io_dtype=io, rot_seed=5)
+    assert api.pages_bytes(big) > 5 << 30
+    far = torch.where(table >= 0, table + (20000 - few), table)
+    pools = api.new_pool(small), api.new_pool(big)
+    fill_random(rng, small, pools[0])
+    size = api.pages_layout(small)[1]
+    pools[1].view(20000, size)[20000 - few:] = pools[0].view(few, size)
+    k, v, q = rows(rng, (2, new, nkv, d), io), rows(rng, (2, new, nkv, d), io), rows(rng, (2, n, 16, d), io)
+    got = []
+    for p, pool, t in ((small, pools[0], table), (big, pools[1], far)):
+        err = i32([0])
+        api.pages_append(p, pool, t, i32(lens), k, v, err=err)
+        now = i32([x + new for x in lens])
+        out, lse = torch.empty_like(q), torch.empty(2, n, 16, device="cuda")
+        ws = api.new_tree_workspace(p, 2, n, 16, t.shape[1])
+        api.tree_attn(p, pool, t, now, q, out, ws, k=k[:, :n].contiguous(), v=v[:, :n].contiguous(), lse=lse)
+        api.check_ws(ws)
+        back = torch.zeros(2, nkv, 940, d, dtype=NP[io], device="cuda")
+        api.pages_read(p, pool, t, now, back, None, err=err)
+        assert int(err) == 0
+        got.append((out, lse, back, pool.view(-1, size)[-few:].clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_rows_past_two_to_the_31_elements(cuda_ok):
+    """Sequences of k, v, q, k_out and rotated heads that lie more than 2^31 elements apart."""
+    rng = np.random.default_rng(98)
+    nkv, d, far = 2, 128, (1 << 31) + 1024
+    store = torch.empty(far + (1 << 20), dtype=torch.bfloat16, device="cuda")
+
+    def apart(x, at):
+        y = store[at:].as_strided(x.shape, (far,) + x.stride()[1:])
+        y.copy_(x)
+        return y
+
+    table, n_pages = make_table(rng, [70, 50], 16)
+    p = api.make_pages(n_pages, 16, nkv, d, 4, 4, rot_seed=5)
+    k, v, q = rows(rng, (2, 30, nkv, d), "bf16"), rows(rng, (2, 30, nkv, d), "bf16"), rows(rng, (2, 30, 4, d), "bf16")
+    k2, v2, q2 = apart(k, 0), apart(v, 1 << 16), apart(q, 1 << 17)
+    assert k2.stride(0) > 1 << 31
+    got = []
+    for a, b, c, at in ((k, v, q, None), (k2, v2, q2, 1 << 18)):
+        pool = api.new_pool(p)
+        api.pages_append(p, pool, table, i32([0, 0]), a, b)
+        out, ws = torch.empty_like(q), api.new_tree_workspace(p, 2, 30, 4, table.shape[1])
+        api.tree_attn(p, pool, table, i32([30, 30]), c, out, ws, k=a, v=b)
+        api.check_ws(ws)
+        back = torch.zeros(2, nkv, 30, d, dtype=torch.bfloat16, device="cuda")
+        if at is not None:
+            back = apart(back, at)
+        api.pages_read(p, pool, table, i32([30, 30]), back, None)
+        got.append((pool, out, back))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    pos, freq = i32([5, 70000]), torch.from_numpy(api.rope_freqs(d, 10000.0)[0]).cuda()
+    want, _ = api.rope(q[:, 0].contiguous(), None, pos, freq)
+    turned, _ = api.rope(q2[:, 0], None, pos, freq, q_out=q2[:, 0])
+    assert torch.equal(turned, want)
+    # one call over more than 2^31 elements, its last tokens as a call of their own
+    n = (far // (8 * d)) + 7
+    x = store[:n * 8 * d].view(n, 8, d)
+    x[-4:] = rows(rng, (4, 8, d), "bf16")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    want, _ = api.rope(x[-4:].clone(), None, pos[-4:].contiguous(), freq)
+    api.rope(x, None, pos, freq, q_out=x)
+    assert torch.equal(x[-4:], want)
