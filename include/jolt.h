@@ -563,7 +563,8 @@ jolt_status jolt_rope_freqs(int32_t rot_dim, double theta, int32_t mode, double 
 /* Per-kernel-family device timing (off by default). When enabled, the library records a CUDA event
  * pair on the launching stream around every launch of the families below and accumulates the
  * elapsed device time together with the launch's algorithmic work (FLOPs of a contraction, or
- * bytes a streaming kernel must move). Host-global; not for concurrent use from several threads. */
+ * bytes a streaming kernel must move). Launches recorded into a graph are left out. Host-global; not for
+ * concurrent use from several threads. */
 typedef enum {
   JOLT_K_GEMM = 0,          /* tcgen05 contractions (compressor, and the decode's value GEMMs) */
   JOLT_K_DECODE_MAIN = 1,   /* decode scores: tcgen05 key rebuild (pre-RoPE) or residual scores,

@@ -43,6 +43,12 @@ StatScope::StatScope(int family, cudaStream_t st, double flops, double bytes, do
     : fam_(family), st_(st), flops_(flops), bytes_(bytes), issued_(issued < 0.0 ? flops : issued) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (!g_on || family < 0) return;  // family < 0: not recorded (the caller's own scope covers it)
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {  // the legacy stream while another is captured
+    cudaGetLastError();
+    return;
+  }
+  if (cs != cudaStreamCaptureStatusNone) return;  // events of a graph cannot be read afterwards
   e0_ = take_event();
   e1_ = take_event();
   if (e0_) cudaEventRecord(e0_, st_);

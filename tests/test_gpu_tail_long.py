@@ -406,3 +406,24 @@ def test_rows_past_two_to_the_31_elements(cuda_ok):
     want, _ = api.rope(x[-4:].clone(), None, pos[-4:].contiguous(), freq)
     api.rope(x, None, pos, freq, q_out=x)
     assert torch.equal(x[-4:], want)
+
+
+def test_kernel_timing_leaves_captured_launches_out(cuda_ok):
+    """Timing is on while a step is captured: the graph runs, and the timing goes on with what is launched outside."""
+    c = attn_case(99, [100], 1, 4, 2, 64, 4, 4, 16, "bf16")
+    p, pool, table, lens, q = c[:5]
+    ws, n = api.new_tree_workspace(p, 1, 1, 4, table.shape[1]), i32(lens)
+    out, want = torch.empty_like(q), run_attn(c[:5] + (None, None, None, None, None))[0]
+    api.stats_read(reset=True)
+    api.stats_enable(True)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            api.tree_attn(p, pool, table, n, q, out, ws)
+        graph.replay()
+        assert torch.equal(out, want)
+        api.tree_attn(p, pool, table, n, q, out, ws)
+        s = api.stats_read(reset=True)
+    finally:
+        api.stats_enable(False)
+    assert s["tree"]["launches"] == 1 and s["tree"]["ms"] > 0
