@@ -427,3 +427,22 @@ def test_kernel_timing_leaves_captured_launches_out(cuda_ok):
     finally:
         api.stats_enable(False)
     assert s["tree"]["launches"] == 1 and s["tree"]["ms"] > 0
+
+
+@pytest.mark.parametrize("io,n", [("bf16", 3), ("bf16", 12), ("bf16", 20), ("bf16", 64), ("f32", 20)])
+@pytest.mark.parametrize("d,b", [(64, 2), (128, 4), (64, 8)])
+def test_value_scales_over_all_of_fp16(cuda_ok, io, n, d, b):
+    """Value scales from 2^-24 to 2^10, constant rows of any size and of zeros, tile after tile."""
+    c = attn_case(100 + b, [1500, 300], n, 2, 2, d, 8, b, 16, io)
+    p, pool = c[0], c[1]
+    off, size = api.pages_layout(p)
+    sz = pool.view(p.n_pages, size)[:, off[3]:off[3] + 2 * 16 * 4].view(torch.float16).view(p.n_pages, 2, 16, 2)
+    rng = np.random.default_rng(b)
+    sz[..., 0] = torch.from_numpy(2.0 ** rng.integers(-24, 11, sz.shape[:3])).half().cuda()
+    sz[..., 1] = torch.from_numpy(rng.standard_normal(sz.shape[:3]) * 2.0 ** rng.integers(-20, 11, sz.shape[:3])).half().cuda()
+    sz[:, :, ::5, 0] = 0.0
+    sz[:, :, 3::7] = 0.0
+    hold(c, tight=False)
+    sz[:] = 0.0  # no value at all
+    out, _ = run_attn(c[:5] + (None, None, None, None, None))
+    assert bool((out == 0).all())
